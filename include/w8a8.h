@@ -341,6 +341,97 @@ W8A8_API int w8a8_moe_g128_forward(const uint16_t* x, const uint16_t* logits, co
                                    const w8a8_moe_g128_debug* dbg, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Dense W8A8 linear with bias, activation and residual in its epilogue.  No
+ * counterpart in the cited sources, which fix only the linear itself: what a
+ * layer does with a projection's output, without another pass over it.
+ *   x  bf16 [M, K], row stride ldx;  qw int8 [N, K];  sw fp32 [N]
+ *   bias fp32 [N] or NULL;  residual bf16 [M, N], row stride ldr, or NULL
+ *   y  bf16 [M, N], row stride ldy
+ *   v[m,n] = (float(sum_k qx[m,k] qw[n,k]) * sx[m]) * sw[n]   as w8a8_linear
+ *   y[m,n] = bf16_rne( residual[m,n] + act( v[m,n] + bias[n] ) )
+ * with one fp32 rounding for each product and sum; the activations are in
+ * fp32 (SILU and GELU_TANH within 2^-20 of their value, GELU = v * Phi(v)).
+ * Strides are in elements and multiples of 8 (ldx >= K, ldr >= N, ldy >= N);
+ * elements of y between N and ldy are not touched.  y may be the residual
+ * itself (same pointer and stride: the residual stream updated in place); it
+ * may not overlap any input otherwise.  ws_bytes >=
+ * w8a8_linear_workspace_size(M, N, K). */
+#define W8A8_ACT_NONE 0
+#define W8A8_ACT_RELU 1
+#define W8A8_ACT_SILU 2        /* v / (1 + e^-v) */
+#define W8A8_ACT_GELU 3        /* v * Phi(v), the normal distribution function */
+#define W8A8_ACT_GELU_TANH 4   /* v * (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */
+W8A8_API int w8a8_linear_epilogue(const uint16_t* x, int64_t ldx, const int8_t* qw, const float* sw, const float* bias,
+                                  int act, const uint16_t* residual, int64_t ldr, uint16_t* y, int64_t ldy, int64_t M,
+                                  int64_t N, int64_t K, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged key-value cache of the attention layers -- [IQ8R] (int8 cache with
+ * one scale per token and head) and [ATOM] "Precision split" (cache in bf16).
+ *   k_cache, v_cache  [num_pages, Hkv, page_size, D], int8 or bf16
+ *   k_scale, v_scale  fp32 [num_pages, Hkv, page_size] for int8 (a value is
+ *                     float(code) * scale); both NULL for bf16
+ * D is 64, 128 or 256; page_size a power of two from 8 to 256; Hkv up to 1024;
+ * num_pages below 2^31.  All of it is one allocation per tensor; offsets are
+ * 64-bit.
+ *
+ * w8a8_kv_append writes T tokens' keys and values:
+ *   k, v   bf16 [T, Hkv, D], token strides ldk, ldv (>= Hkv * D, multiples of 8)
+ *   slots  int64 [T]: page * page_size + position in the page; a negative slot
+ *          skips its token (padding).  Slots of one call are distinct.
+ * int8: per (token, head) s = max|x| / 127, q = clamp(rne(x / s), -127, 127),
+ * the rule of w8a8_quant_act; a zero row has s = 0, codes 0.  bf16: a copy.
+ * A slot past the cache writes nothing and records W8A8_ERR_INVALID_ARG in
+ * the device error word. */
+W8A8_API int w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, void* k_cache,
+                            void* v_cache, float* k_scale, float* v_scale, const int64_t* slots, int64_t T, int Hkv,
+                            int D, int64_t num_pages, int page_size, void* stream);
+
+/* Attention of one new token per sequence over the paged cache:
+ *   q  bf16 [B, Hq, D], sequence stride ldq (>= Hq * D, a multiple of 8);
+ *      query head h reads key-value head h / (Hq / Hkv)  (Hq % Hkv == 0)
+ *   block_table  int32 [B, max_pages], row stride ld_table: page of each
+ *      page_size positions; only the first ceil(length / page_size) entries
+ *      of a row are read
+ *   lengths  int32 [B]: positions that the token attends to, itself included
+ *   y  bf16 [B, Hq, D], dense
+ *   l_t = scale * (q . k_t),  p_t = exp(l_t - max l),
+ *   y = bf16_rne( sum_t p_t v_t / sum_t p_t )   for t < lengths[b]
+ * Scores, maxima, sums and outputs are held in fp32.  A sequence of length 0
+ * (or less) gives zeros.  A length beyond max_pages * page_size is cut there,
+ * and positions of a page number outside [0, num_pages) count as absent;
+ * either records W8A8_ERR_INVALID_ARG in the device error word.
+ * The context is split over the GPU and its parts are joined in a fixed order:
+ * the same call gives the same bits again.  1 <= B <= 4096.
+ * ws_bytes >= w8a8_paged_attention_workspace_size(B, Hq, Hkv, D). */
+W8A8_API size_t w8a8_paged_attention_workspace_size(int64_t B, int Hq, int Hkv, int D);
+W8A8_API int w8a8_paged_attention(const uint16_t* q, int64_t ldq, const void* k_cache, const void* v_cache,
+                                  const float* k_scale, const float* v_scale, const int32_t* block_table,
+                                  int64_t ld_table, const int32_t* lengths, uint16_t* y, int64_t B, int Hq, int Hkv,
+                                  int D, int64_t num_pages, int page_size, int64_t max_pages, float scale, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Log probabilities from the head's logits: of given tokens, the entropy of
+ * the distribution, and the most likely alternatives.
+ *   logits  [M, V], row stride ld >= V elements, any element alignment;
+ *           bf16 (logits_f32 = 0) or fp32 (logits_f32 = 1)
+ *   tokens  int32 [M, G] or NULL (G = 0): the given tokens of each row
+ *   logprob fp32 [M, G]: x_tok - lse;  NaN for a token outside [0, V)
+ *   entropy fp32 [M] or NULL: -sum_i p_i log p_i, nats
+ *   top_ids int32 [M, topk], top_logprobs fp32 [M, topk] (topk = 0: none):
+ *           descending logits, ties to the lower index; 0 <= topk <= 32,
+ *           topk <= V
+ * with lse = max x + log sum_i exp(x_i - max x) in fp32.  A logit of -inf
+ * (masked) has probability 0 and adds nothing to the entropy; where every
+ * logit of a row is -inf, every log probability is -inf and the entropy 0.
+ * A NaN or +inf logit makes the row's log probabilities and entropy NaN
+ * (NaN logits rank as -inf in the alternatives). */
+W8A8_API int w8a8_token_logprobs(const void* logits, int logits_f32, int64_t ld, const int32_t* tokens, int G,
+                                 float* logprob, float* entropy, int32_t* top_ids, float* top_logprobs, int64_t M,
+                                 int64_t V, int topk, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Diagnostics. */
 
 /* The library's fp32 exponential (Cody & Waite reduction, degree-7 Taylor),

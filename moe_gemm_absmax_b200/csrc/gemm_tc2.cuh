@@ -59,7 +59,8 @@ struct Tc2Smem {
     static constexpr int kEpiOff = kTiles + (kBars + 16 + 15) / 16 * 16;
     static constexpr int kEpiBytes = kTc2Epi * BN * 4;
     static constexpr int kBytes = 1024 + kEpiOff + kEpiBytes;
-    static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
+    static constexpr int kBytesFused = kBytes + kEpiBytes;   // kEpiFused: the same again for the biases
+    static_assert(kBytesFused <= 227 * 1024, "shared memory per CTA");
 };
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -130,7 +131,7 @@ __device__ __forceinline__ void tc2_commit_pair(uint64_t* bar) {
 template <int EPI, int BN = 256>
 __global__ void __launch_bounds__(kTc2Threads, 1)
     gemm_i8_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, TcParams p) {
-    static_assert(EPI == kEpiBf16 || EPI == kEpiS32 || EPI == kEpiMoeGated, "dense epilogues");
+    static_assert(EPI == kEpiBf16 || EPI == kEpiS32 || EPI == kEpiMoeGated || EPI == kEpiFused, "dense epilogues");
     static_assert(BN % 16 == 0 && (BN / 2) % 8 == 0 && BN <= 256, "pair tile width");
     constexpr int kCols = 2 * BN <= 256 ? 256 : 512;   // two accumulators of BN columns (a power of two)
     using SM = Tc2Smem<BN>;
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
         const int chalf = (warp - 2) >> 2;         // chunks c = 32 chalf + 64 i
         const uint32_t tempty_leader0 = mapa_shared(smem_u32(&tempty[0]), 0);
         float* sw_s = epi_scratch + (warp - 2) * BN;   // this warp's copy of the tile's column scales
+        float* bias_s = sw_s + SM::kEpiBytes / 4;      // kEpiFused: and of its biases
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int tile = cluster_id; tile < num_tiles; tile += nclusters) {
@@ -282,8 +284,8 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
             const int row = mt * kTc2BM + (int)rank * 128 + quarter * 32 + lane;
             const bool row_ok = row < p.M;
             float sxr = 0.0f;
-            if ((EPI == kEpiBf16 || EPI == kEpiMoeGated) && row_ok) sxr = __ldg(p.sx + row);
-            if (EPI == kEpiBf16 || EPI == kEpiMoeGated) {
+            if ((EPI == kEpiBf16 || EPI == kEpiMoeGated || EPI == kEpiFused) && row_ok) sxr = __ldg(p.sx + row);
+            if (EPI == kEpiBf16 || EPI == kEpiMoeGated || EPI == kEpiFused) {
                 // the tile's BN column scales (N % 8 == 0: a 4-column vector is all in or all out)
                 __syncwarp();   // the previous tile's reads are done
                 for (int v = lane; v < BN / 4; v += 32) {
@@ -291,20 +293,44 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
                     float4 sv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     if (n < p.N) sv = __ldg(reinterpret_cast<const float4*>(p.sw + n));
                     *reinterpret_cast<float4*>(sw_s + 4 * v) = sv;
+                    if (EPI == kEpiFused) {
+                        float4 bv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (p.f.bias && n < p.N) bv = __ldg(reinterpret_cast<const float4*>(p.f.bias + n));
+                        *reinterpret_cast<float4*>(bias_s + 4 * v) = bv;
+                    }
                 }
                 __syncwarp();
             }
+            // residual of one 32-column chunk, in flight with the chunk's TMEM load
+            auto load_res = [&](uint4 (&q)[4], int c) {
+                if (EPI != kEpiFused) return;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    q[v] = make_uint4(0, 0, 0, 0);
+                    if (p.f.res && row_ok && c + v * 8 < BN && nt * BN + c + v * 8 < p.N)
+                        q[v] = ld_residual16(p.f.res + (int64_t)row * p.f.ldr + nt * BN + c + v * 8);
+                }
+            };
+            uint4 qa[4], qb[4];
+            load_res(qa, 32 * chalf);
             if (!mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, (kKernelIdGemmTc2 << 16) | 6)) break;
             tc_fence_after();
             const uint32_t tq = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN);
             // one 32-column chunk: convert and store (the next chunk's TMEM load is in flight)
-            auto chunk = [&](const uint32_t (&r)[32], int c) {
+            auto chunk = [&](const uint32_t (&r)[32], const uint4 (&q)[4], int c) {
                 const int n0 = nt * BN + c;
                 if (!row_ok || n0 >= p.N) return;
                 // the tile's columns in this chunk (BN % 32 == 16: the last chunk holds
                 // 16; its TMEM load reads 16 columns past the tile, which are ignored)
                 const int ncol = BN - c < 32 ? BN - c : 32;
-                if (EPI == kEpiBf16) {
+                if (EPI == kEpiFused) {
+                    uint16_t* yrow = reinterpret_cast<uint16_t*>(p.out) + (int64_t)row * p.f.ldy;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (v * 8 < ncol && n0 + v * 8 < p.N)
+                            *reinterpret_cast<uint4*>(yrow + n0 + v * 8) =
+                                epi_fused8(r + v * 8, sxr, sw_s + c + v * 8, bias_s + c + v * 8, q[v], p.f.act);
+                } else if (EPI == kEpiBf16) {
                     uint16_t* yrow = reinterpret_cast<uint16_t*>(p.out) + (int64_t)row * p.N;
                     const uint64_t sx2 = f2_pack(sxr, sxr);
 #pragma unroll
@@ -356,13 +382,19 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
             if (c < BN) tmem_ld_32x32b_x32(tq + (uint32_t)c, ra);
             while (c < BN) {
                 tc_wait_ld();
-                if (c + 64 < BN) tmem_ld_32x32b_x32(tq + (uint32_t)(c + 64), rb);
-                chunk(ra, c);
+                if (c + 64 < BN) {
+                    tmem_ld_32x32b_x32(tq + (uint32_t)(c + 64), rb);
+                    load_res(qb, c + 64);
+                }
+                chunk(ra, qa, c);
                 c += 64;
                 if (c >= BN) break;
                 tc_wait_ld();
-                if (c + 64 < BN) tmem_ld_32x32b_x32(tq + (uint32_t)(c + 64), ra);
-                chunk(rb, c);
+                if (c + 64 < BN) {
+                    tmem_ld_32x32b_x32(tq + (uint32_t)(c + 64), ra);
+                    load_res(qa, c + 64);
+                }
+                chunk(rb, qb, c);
                 c += 64;
             }
             tc_fence_before();

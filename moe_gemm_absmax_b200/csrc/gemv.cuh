@@ -28,6 +28,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "epilogue.cuh"
 
 namespace w8a8 {
 
@@ -223,12 +224,13 @@ struct GemvEpiDense {
     void* out;         // bf16 [M,N] or int32 [M,N]
     int M, N;
     int s32;           // 1: raw int32
+    EpiFused f;        // FUSED: bias, activation, residual and row strides (epilogue.cuh)
 };
 
 // MINB: resident CTAs per SM the register budget is sized for (4: 64
 // registers a thread, 32 warps an SM) -- the decode weight stream needs many
 // warps per SM with a few loads each, more than few warps with many loads.
-template <int WN, int WK, int TG, int U, int MINB = 1>
+template <int WN, int WK, int TG, int U, int MINB = 1, bool FUSED = false>
 __global__ void __launch_bounds__(kGemvThreads, MINB) gemv_dense_kernel(GemvShape a, GemvEpiDense e) {
     int acc[TG][4];
     int block;
@@ -241,7 +243,10 @@ __global__ void __launch_bounds__(kGemvThreads, MINB) gemv_dense_kernel(GemvShap
             const int m = tg * 8 + 2 * t + (j & 1);
             const int n = block * 16 + g + (j >> 1) * 8;
             if (m < e.M && n < e.N) {
-                if (e.s32) {
+                if (FUSED) {
+                    reinterpret_cast<uint16_t*>(e.out)[m * e.f.ldy + n] =
+                        epi_fused1(acc[tg][j], __ldcg(e.sx + m), __ldg(e.sw + n), e.f, m, n);
+                } else if (e.s32) {
                     reinterpret_cast<int32_t*>(e.out)[(int64_t)m * e.N + n] = acc[tg][j];
                 } else {
                     const float v = __fmul_rn(__fmul_rn(__int2float_rn(acc[tg][j]), __ldcg(e.sx + m)), __ldg(e.sw + n));

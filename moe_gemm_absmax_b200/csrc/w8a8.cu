@@ -10,12 +10,14 @@
 #include <atomic>
 #include <mutex>
 
+#include "attention.cuh"
 #include "common.cuh"
 #include "fwht.cuh"
 #include "gemm_tc.cuh"
 #include "gemm_tc2.cuh"
 #include "gemv.cuh"
 #include "gemv_tc.cuh"
+#include "logprobs.cuh"
 #include "moe.cuh"
 #include "moe_g128.cuh"
 #include "moe_swap.cuh"
@@ -90,12 +92,13 @@ template <int BN, int STAGES, int EPI, int NACC, int NEPI = 4>
 int launch_tc(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st) {
     using SM = TcSmem<BN, STAGES>;
     auto kern = gemm_i8_tc_kernel<BN, STAGES, EPI, NACC, false, NEPI>;
+    constexpr int kBytes = EPI == kEpiFused ? SM::kBytesFused : SM::kBytes;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return W8A8_ERR_CUDA;
     static bool attr_done[kMaxDevices] = {false};
     if (dev >= kMaxDevices) return W8A8_ERR_UNSUPPORTED;
     if (!attr_done[dev]) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes) != cudaSuccess)
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
             return W8A8_ERR_CUDA;
         attr_done[dev] = true;
     }
@@ -107,7 +110,7 @@ int launch_tc(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st) {
     p.num_k_blocks = (p.K + kTcBK - 1) / kTcBK;
     const int tiles = p.num_m_tiles * p.num_n_tiles;
     const int grid = tiles < device_sms(dev) ? tiles : device_sms(dev);
-    kern<<<grid, tc_threads<NEPI>(), SM::kBytes, st>>>(ta, tb, p);
+    kern<<<grid, tc_threads<NEPI>(), kBytes, st>>>(ta, tb, p);
     return last_launch_status();
 }
 
@@ -116,13 +119,14 @@ template <int EPI, int BN>
 int launch_tc2_bn(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st) {
     using SM = Tc2Smem<BN>;
     auto kern = gemm_i8_tc2_kernel<EPI, BN>;
+    constexpr int kBytes = EPI == kEpiFused ? SM::kBytesFused : SM::kBytes;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return W8A8_ERR_CUDA;
     if (dev < 0 || dev >= kMaxDevices) return W8A8_ERR_UNSUPPORTED;
     static int max_clusters[kMaxDevices] = {0};
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kTc2Threads, 1, 1);
-    cfg.dynamicSmemBytes = SM::kBytes;
+    cfg.dynamicSmemBytes = kBytes;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -132,7 +136,7 @@ int launch_tc2_bn(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st)
     cfg.attrs = at;
     cfg.numAttrs = 1;
     if (max_clusters[dev] == 0) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes) != cudaSuccess)
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
             return W8A8_ERR_CUDA;
         cfg.gridDim = dim3((unsigned)(2 * (device_sms(dev) / 2)), 1, 1);
         int n = 0;
@@ -231,7 +235,7 @@ int pick_bn(int64_t M, int64_t N, int sms) {
 constexpr int64_t kTc2MinM = 256;
 
 int run_tc(const int8_t* qx, const float* sx, const int8_t* qw, const float* sw, void* out, int64_t M, int64_t N,
-           int64_t K, int epi, cudaStream_t st) {
+           int64_t K, int epi, cudaStream_t st, const EpiFused* fused = nullptr) {
     TcParams p = {};
     p.M = (int)M;
     p.N = (int)N;
@@ -239,6 +243,12 @@ int run_tc(const int8_t* qx, const float* sx, const int8_t* qw, const float* sw,
     p.sx = sx;
     p.sw = sw;
     p.out = out;
+    if (epi == kEpiFused) {
+        p.f = *fused;
+        if (M >= kTc2MinM) return launch_tc2<kEpiFused>(qx, qw, p, st);
+        return pick_bn(M, N, current_sms()) == 256 ? launch_tc<256, 4, kEpiFused, 2>(qx, qw, p, st)
+                                                   : launch_tc<128, 6, kEpiFused, 2>(qx, qw, p, st);
+    }
     if (M >= kTc2MinM) return epi == kEpiBf16 ? launch_tc2<kEpiBf16>(qx, qw, p, st) : launch_tc2<kEpiS32>(qx, qw, p, st);
     const int bn = pick_bn(M, N, current_sms());
     if (epi == kEpiBf16)
@@ -361,7 +371,7 @@ int launch_gemv_tc(const int8_t* qx, const int8_t* qw, const GemvTc& a, const Ge
     return cuda_status(cudaLaunchKernelEx(&cfg, kern, tw, tx, args));
 }
 
-template <int TG, int U>
+template <int TG, int U, bool FUSED = false>
 int launch_gemv_reg(const GemvShape& a, const GemvEpiDense& e, const GemvPlan& g, bool after_quant, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)g.ctas_x, (unsigned)g.nkseg, 1);
@@ -371,9 +381,9 @@ int launch_gemv_reg(const GemvShape& a, const GemvEpiDense& e, const GemvPlan& g
     pdl_config(cfg, at, after_quant);
     GemvShape args = a;
     args.trig = g.trig;
-    auto kern = g.wn == 4 ? gemv_dense_kernel<4, 2, TG, U, kGemvMinBlocks>
-              : g.wn == 2 ? gemv_dense_kernel<2, 4, TG, U, kGemvMinBlocks>
-                          : gemv_dense_kernel<1, 8, TG, U, kGemvMinBlocks>;
+    auto kern = g.wn == 4 ? gemv_dense_kernel<4, 2, TG, U, kGemvMinBlocks, FUSED>
+              : g.wn == 2 ? gemv_dense_kernel<2, 4, TG, U, kGemvMinBlocks, FUSED>
+                          : gemv_dense_kernel<1, 8, TG, U, kGemvMinBlocks, FUSED>;
     return cuda_status(cudaLaunchKernelEx(&cfg, kern, args, e));
 }
 
@@ -410,7 +420,8 @@ int launch_gemv_gated(const int8_t* qx, const float* sx, const int8_t* qw, const
 
 // Runs the GEMV; `scratch` holds the partials and the counters (zero on entry).
 int run_gemv(const int8_t* qx, const float* sx, const int8_t* qw, const float* sw, void* out, int64_t M, int64_t N,
-             int64_t K, bool s32, const GemvPlan& g, void* scratch, bool after_quant, cudaStream_t st) {
+             int64_t K, bool s32, const GemvPlan& g, void* scratch, bool after_quant, cudaStream_t st,
+             const EpiFused* fused = nullptr) {
     if (!g.tc) {
         GemvShape a;
         a.w = qw;
@@ -428,6 +439,11 @@ int run_gemv(const int8_t* qx, const float* sx, const int8_t* qw, const float* s
         e.M = (int)M;
         e.N = (int)N;
         e.s32 = s32 ? 1 : 0;
+        if (fused) {
+            e.f = *fused;
+            return launch_gemv_reg<1, kGemvUnrollDecode, true>(a, e, g, after_quant, st);
+        }
+        e.f = {};
         return launch_gemv_reg<1, kGemvUnrollDecode>(a, e, g, after_quant, st);
     }
     GemvTc a;
@@ -743,6 +759,40 @@ int w8a8_linear(const uint16_t* x, const int8_t* qw, const float* sw, uint16_t* 
     if (e != cudaSuccess) return W8A8_ERR_CUDA;
     if (gemv) return run_gemv(qx, sx, qw, sw, y, M, N, K, false, g, scratch, true, st);
     return run_tc(qx, sx, qw, sw, y, M, N, K, kEpiBf16, st);
+}
+
+int w8a8_linear_epilogue(const uint16_t* x, int64_t ldx, const int8_t* qw, const float* sw, const float* bias, int act,
+                         const uint16_t* residual, int64_t ldr, uint16_t* y, int64_t ldy, int64_t M, int64_t N,
+                         int64_t K, void* ws, size_t ws_bytes, void* stream) {
+    if (!x || !qw || !sw || !y || !ws) return W8A8_ERR_INVALID_ARG;
+    if (!gemm_shape_ok(M, N, K)) return W8A8_ERR_INVALID_ARG;
+    if (act < W8A8_ACT_NONE || act > W8A8_ACT_GELU_TANH) return W8A8_ERR_INVALID_ARG;
+    if (ldx < K || ldx % 8 != 0 || ldy < N || ldy % 8 != 0) return W8A8_ERR_INVALID_ARG;
+    if (residual && (ldr < N || ldr % 8 != 0 || !aligned(residual, 16))) return W8A8_ERR_INVALID_ARG;
+    if (residual == y && ldr != ldy) return W8A8_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(qw, 16) || !aligned(sw, 16) || !aligned(bias, 16) || !aligned(y, 16) ||
+        !aligned(ws, 256))
+        return W8A8_ERR_INVALID_ARG;
+    if (ws_bytes < w8a8_linear_workspace_size(M, N, K)) return W8A8_ERR_WORKSPACE;
+    if (K / 8 > (int64_t)8 * 256 * kQuantMaxVec) return W8A8_ERR_UNSUPPORTED;
+    cudaStream_t st = (cudaStream_t)stream;
+    int8_t* qx = reinterpret_cast<int8_t*>(ws);
+    float* sx = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + align_up((size_t)M * K, 256));
+    void* scratch = reinterpret_cast<uint8_t*>(sx) + align_up((size_t)M * 4, 256);
+    const bool gemv = M <= 8;
+    GemvPlan g = gemv_plan(M, N, K);
+    int* ctr = gemv ? gemv_counters(g, scratch) : nullptr;
+    EpiFused f;
+    f.bias = bias;
+    f.res = residual;
+    f.ldr = ldr;
+    f.ldy = ldy;
+    f.act = act;
+    if (launch_quant_rows<uint16_t>(x, M, K, ldx, qx, K, sx, st, current_sms(), ctr, ctr ? gemv_counter_count(g) : 0,
+                                    true) != cudaSuccess)
+        return W8A8_ERR_CUDA;
+    if (gemv) return run_gemv(qx, sx, qw, sw, y, M, N, K, false, g, scratch, true, st, &f);
+    return run_tc(qx, sx, qw, sw, y, M, N, K, kEpiFused, st, &f);
 }
 
 // ----------------------------------------------------------------- linear without caller workspace
@@ -1483,6 +1533,194 @@ int w8a8_linear_trunk(const int8_t* qx, const uint16_t* sx, const int8_t* qw, co
                       uint16_t* y, int64_t M, int64_t N, int64_t K, void* stream) {
     if (!su8 || !s2) return W8A8_ERR_INVALID_ARG;
     return linear_group_scaled(qx, sx, qw, nullptr, y, M, N, K, 0.0078125f, (cudaStream_t)stream, su8, s2);
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------- paged cache
+namespace {
+int log2_exact(int v) {
+    int s = 0;
+    while ((1 << s) < v) ++s;
+    return (1 << s) == v ? s : -1;
+}
+
+bool cache_shape_ok(int Hkv, int D, int64_t num_pages, int page_size) {
+    return (D == 64 || D == 128 || D == 256) && page_size >= 8 && page_size <= 256 && log2_exact(page_size) >= 0 &&
+           Hkv <= 1024 && num_pages < (int64_t)1 << 31;
+}
+
+// Query tiles a pass and CTAs per SM by the registers a thread needs: output
+// sums NQ * D / 4, a tile's keys and values, the query.
+constexpr int attn_minb(int D, bool int8, int nq) {
+    return D == 256 ? 2 : (nq == 2 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 3));
+}
+// 16 query heads a pass where more than 8 share a key-value head, except at
+// D = 256, whose output sums would not fit the register file.
+int attn_nq(int G, int D) { return G > 8 && D < 256 ? 2 : 1; }
+constexpr int kAttnSms = 148;   // the work split's grid is fixed, so that workspace sizes are
+
+size_t attn_part_rows(int D, int nq) { return (size_t)kAttnSms * attn_minb(D, true, nq) * 2 * 8 * nq; }
+
+template <int D, bool INT8, int NQ>
+int launch_attn(AttnArgs a, cudaStream_t st) {
+    constexpr int kMinB = attn_minb(D, INT8, NQ);
+    constexpr int CH = kAttnWarps * attn_tt<D, INT8>();
+    const int64_t heads = (int64_t)a.Hkv * a.qtiles;
+    const int64_t most = (int64_t)a.B * heads * ((a.cap + CH - 1) / CH);   // chunks, if every sequence were full
+    a.grid = (int)(most < kAttnSms * kMinB ? (most > 0 ? most : 1) : kAttnSms * kMinB);
+    paged_attention_kernel<D, INT8, NQ, kMinB><<<(unsigned)a.grid, kAttnThreads, 0, st>>>(a);
+    int rc = last_launch_status();
+    if (rc != W8A8_OK) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.B * heads), 1, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    pdl_config(cfg, at, true);
+    return cuda_status(cudaLaunchKernelEx(&cfg, attn_join_kernel<D, CH, NQ>, a));
+}
+
+template <int D, bool INT8>
+int launch_attn_nq(const AttnArgs& a, cudaStream_t st) {
+    if constexpr (D < 256) {
+        if (attn_nq(a.G, D) == 2) return launch_attn<D, INT8, 2>(a, st);
+    }
+    return launch_attn<D, INT8, 1>(a, st);
+}
+
+template <int D, bool INT8>
+int launch_append(const KvAppendArgs& a, cudaStream_t st) {
+    const int64_t threads = a.T * a.Hkv * (D / 8);
+    kv_append_kernel<D, INT8><<<dim3((unsigned)((threads + 255) / 256), 2, 1), 256, 0, st>>>(a);
+    return last_launch_status();
+}
+}  // namespace
+
+extern "C" {
+
+int w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, void* k_cache, void* v_cache,
+                   float* k_scale, float* v_scale, const int64_t* slots, int64_t T, int Hkv, int D, int64_t num_pages,
+                   int page_size, void* stream) {
+    if (!k || !v || !k_cache || !v_cache || !slots || T <= 0 || Hkv <= 0 || num_pages <= 0)
+        return W8A8_ERR_INVALID_ARG;
+    if ((k_scale == nullptr) != (v_scale == nullptr)) return W8A8_ERR_INVALID_ARG;
+    if (!cache_shape_ok(Hkv, D, num_pages, page_size) || T > (int64_t)1 << 30) return W8A8_ERR_UNSUPPORTED;
+    if (ldk < (int64_t)Hkv * D || ldv < (int64_t)Hkv * D || ldk % 8 != 0 || ldv % 8 != 0) return W8A8_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 8) ||
+        !aligned(v_scale, 8) || !aligned(slots, 8))
+        return W8A8_ERR_INVALID_ARG;
+    if (T * Hkv * (D / 8) / 256 >= 0x7fffffffLL) return W8A8_ERR_UNSUPPORTED;
+    KvAppendArgs a;
+    a.k = {k, ldk, k_cache, k_scale};
+    a.v = {v, ldv, v_cache, v_scale};
+    a.slots = slots;
+    a.T = T;
+    a.num_pages = num_pages;
+    a.Hkv = Hkv;
+    a.page_shift = log2_exact(page_size);
+    cudaStream_t st = (cudaStream_t)stream;
+    if (k_scale)
+        return D == 64 ? launch_append<64, true>(a, st) : D == 128 ? launch_append<128, true>(a, st)
+                                                                   : launch_append<256, true>(a, st);
+    return D == 64 ? launch_append<64, false>(a, st) : D == 128 ? launch_append<128, false>(a, st)
+                                                                : launch_append<256, false>(a, st);
+}
+
+size_t w8a8_paged_attention_workspace_size(int64_t B, int Hq, int Hkv, int D) {
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128 && D != 256)) return 0;
+    const size_t rows = attn_part_rows(D, attn_nq(Hq / Hkv, D));
+    return align_up(rows * D * 4, 256) + align_up(rows * 8, 256);
+}
+
+int w8a8_paged_attention(const uint16_t* q, int64_t ldq, const void* k_cache, const void* v_cache,
+                         const float* k_scale, const float* v_scale, const int32_t* block_table, int64_t ld_table,
+                         const int32_t* lengths, uint16_t* y, int64_t B, int Hq, int Hkv, int D, int64_t num_pages,
+                         int page_size, int64_t max_pages, float scale, void* ws, size_t ws_bytes, void* stream) {
+    if (!q || !k_cache || !v_cache || !block_table || !lengths || !y || !ws) return W8A8_ERR_INVALID_ARG;
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || num_pages <= 0 || max_pages <= 0 || ld_table < max_pages)
+        return W8A8_ERR_INVALID_ARG;
+    if ((k_scale == nullptr) != (v_scale == nullptr)) return W8A8_ERR_INVALID_ARG;
+    if (!cache_shape_ok(Hkv, D, num_pages, page_size) || B > kAttnMaxB || max_pages >= (int64_t)1 << 31 ||
+        Hq > (1 << 16))
+        return W8A8_ERR_UNSUPPORTED;
+    if (ldq < (int64_t)Hq * D || ldq % 8 != 0) return W8A8_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 8) ||
+        !aligned(v_scale, 8) || !aligned(block_table, 4) || !aligned(lengths, 4) || !aligned(y, 16) || !aligned(ws, 256))
+        return W8A8_ERR_INVALID_ARG;
+    if (ws_bytes < w8a8_paged_attention_workspace_size(B, Hq, Hkv, D)) return W8A8_ERR_WORKSPACE;
+    AttnArgs a;
+    a.q = q;
+    a.ldq = ldq;
+    a.kc = k_cache;
+    a.vc = v_cache;
+    a.ks = k_scale;
+    a.vs = v_scale;
+    a.table = block_table;
+    a.ld_table = ld_table;
+    a.lengths = lengths;
+    a.y = y;
+    a.B = (int)B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    const int nq = attn_nq(a.G, D);
+    a.qtiles = (a.G + 8 * nq - 1) / (8 * nq);
+    a.num_pages = num_pages;
+    a.page_shift = log2_exact(page_size);
+    a.cap = max_pages << a.page_shift;
+    a.scale_log2 = scale * kLog2e;
+    const size_t rows = attn_part_rows(D, nq);
+    a.part_o = reinterpret_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(ws) + align_up(rows * D * 4, 256));
+    a.grid = 0;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (k_scale)
+        return D == 64 ? launch_attn_nq<64, true>(a, st) : D == 128 ? launch_attn_nq<128, true>(a, st)
+                                                                    : launch_attn_nq<256, true>(a, st);
+    return D == 64 ? launch_attn_nq<64, false>(a, st) : D == 128 ? launch_attn_nq<128, false>(a, st)
+                                                                 : launch_attn_nq<256, false>(a, st);
+}
+
+// ----------------------------------------------------------------- log probabilities
+int w8a8_token_logprobs(const void* logits, int logits_f32, int64_t ld, const int32_t* tokens, int G, float* logprob,
+                        float* entropy, int32_t* top_ids, float* top_logprobs, int64_t M, int64_t V, int topk,
+                        void* stream) {
+    if (!logits || M <= 0 || V <= 0 || ld < V || G < 0 || topk < 0 || topk > V) return W8A8_ERR_INVALID_ARG;
+    if (logits_f32 != 0 && logits_f32 != 1) return W8A8_ERR_INVALID_ARG;
+    if (G > 0 && (!tokens || !logprob)) return W8A8_ERR_INVALID_ARG;
+    if (topk > 0 && (!top_ids || !top_logprobs)) return W8A8_ERR_INVALID_ARG;
+    if (!aligned(logits, logits_f32 ? 4 : 2) || !aligned(tokens, 4) || !aligned(logprob, 4) || !aligned(entropy, 4) ||
+        !aligned(top_ids, 4) || !aligned(top_logprobs, 4))
+        return W8A8_ERR_INVALID_ARG;
+    if (topk > kLpMaxTop || V > (int64_t)1 << 30 || M > (int64_t)1 << 27 || G > (1 << 20)) return W8A8_ERR_UNSUPPORTED;
+    LpArgs a;
+    a.logits = logits;
+    a.ld = ld;
+    a.tokens = tokens;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.V = (int)V;
+    a.G = G;
+    a.topk = topk;
+    const int64_t windows = (V * (logits_f32 ? 4 : 2) + 15) / 16;
+    int C = 8;
+    while (C > 1 && (M * C > 2 * current_sms() || windows < (int64_t)C * kLpThreads)) C /= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(M * C), 1, 1);
+    cfg.blockDim = dim3(kLpThreads, 1, 1);
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)C;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cuda_status(logits_f32 ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<float>, a)
+                                  : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<uint16_t>, a));
 }
 
 // ----------------------------------------------------------------- diagnostics

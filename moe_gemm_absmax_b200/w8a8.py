@@ -9,6 +9,7 @@ no CPU path.  If the library has not been built, :func:`lib` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -27,6 +28,8 @@ EXPORTS = (
     "w8a8_moe_forward", "w8a8_moe_set_combine", "w8a8_moe_g128_workspace_size", "w8a8_moe_g128_forward", "w8a8_mlp_workspace_size", "w8a8_mlp_forward", "fwht128_quant", "w8a8_linear_g128",
     "group128_quant", "w8a8_linear_group128", "w8a8_trunk_weight_quant", "w8a8_linear_trunk",
     "w8a8_shared_expert_workspace_size", "w8a8_shared_expert_forward",
+    "w8a8_linear_epilogue", "w8a8_kv_append", "w8a8_paged_attention_workspace_size", "w8a8_paged_attention",
+    "w8a8_token_logprobs",
     "w8a8_exp_proj",
     "w8a8_get_device_error", "w8a8_debug_wait_timeout", "w8a8_status_str", "w8a8_version",
 )
@@ -68,7 +71,7 @@ def lib() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"libw8a8.so not built ({LIB_PATH}); run moe_gemm_absmax_b200.build.build()")
     L = ctypes.CDLL(LIB_PATH)
-    vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+    vp, i64, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
     sig = {
         "w8a8_quant_act": ([vp, i64, i64, i64, vp, vp, vp], i32),
         "w8a8_quant_rows_f32": ([vp, i64, i64, vp, vp, vp], i32),
@@ -97,6 +100,12 @@ def lib() -> ctypes.CDLL:
         "w8a8_shared_expert_workspace_size": ([i64, i32, i32], sz),
         "w8a8_shared_expert_forward": ([vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, vp, sz,
                                         ctypes.POINTER(SharedExpertDebug), vp], i32),
+        "w8a8_linear_epilogue": ([vp, i64, vp, vp, vp, i32, vp, i64, vp, i64, i64, i64, i64, vp, sz, vp], i32),
+        "w8a8_kv_append": ([vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, i32, i32, i64, i32, vp], i32),
+        "w8a8_paged_attention_workspace_size": ([i64, i32, i32, i32], sz),
+        "w8a8_paged_attention": ([vp, i64, vp, vp, vp, vp, vp, i64, vp, vp, i64, i32, i32, i32, i64, i32, i64, f32, vp,
+                                  sz, vp], i32),
+        "w8a8_token_logprobs": ([vp, i32, i64, vp, i32, vp, vp, vp, vp, i64, i64, i32, vp], i32),
         "w8a8_exp_proj": ([vp, vp, i64, vp], i32),
         "w8a8_get_device_error": ([vp, ctypes.POINTER(ctypes.c_int)], i32),
         "w8a8_debug_wait_timeout": ([i64, vp], i32),
@@ -500,6 +509,188 @@ def shared_expert_forward(x, w13, u13, r13, w2, s2, y=None, ws=None, debug: bool
                                             M, H, I, _ptr(ws), ws.numel(), dbg_p, _stream(stream)),
            "w8a8_shared_expert_forward")
     return (y, dbg_t) if debug else y
+
+
+# ------------------------------------------------------------------ linear with an epilogue
+
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
+
+
+def _placed(fn):
+    """Runs fn with the device of its first tensor current and, where a stream is given, on that stream: what fn
+    allocates then belongs to the stream that uses it, so the caching allocator cannot hand it on too early."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kwargs):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise TypeError(f"{fn.__name__}: the first argument must be a CUDA tensor")
+        if stream is not None:
+            if stream.device != first.device:
+                raise ValueError("stream is on another device than the tensors")
+            with torch.cuda.stream(stream):
+                return fn(first, *args, **kwargs)
+        if first.device.index != torch.cuda.current_device():
+            with torch.cuda.device(first.device):
+                return fn(first, *args, **kwargs)
+        return fn(first, *args, **kwargs)
+    return call
+
+
+def _on(t, dtype, name, shape, device):
+    """Contiguous tensor of this type, shape and device."""
+    _need(t, dtype, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _row_stride(t, dtype, name, device, shape=None, ndim=2) -> int:
+    """Row stride of a tensor whose rows (all but the first dim) are dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != ndim or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have shape {tuple(shape) if shape is not None else f'({ndim} dims)'}, "
+                         f"got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    n = 1
+    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and step != n:
+            raise ValueError(f"{name}: all but the first dim must be dense")
+        n *= size
+    return t.stride(0) if t.shape[0] > 1 else n
+
+
+@_placed
+def linear_epilogue(x, qw, sw, bias=None, act: int = ACT_NONE, residual=None, y=None, ws=None) -> torch.Tensor:
+    """Online W8A8 linear with its epilogue: y = residual + act(linear(x) + bias), rounded to bf16 once.
+
+    x bf16 [M,K]; qw int8 [N,K], sw fp32 [N]; bias fp32 [N]; residual and y bf16 [M,N].  x, residual and y may be
+    row-strided (unit column stride, row strides a multiple of 8); y may be the residual itself.  act is one of
+    ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH.  stream= as in the other calls."""
+    dev = x.device
+    ldx = _row_stride(x, torch.bfloat16, "x", dev)
+    M, K = x.shape
+    if not isinstance(qw, torch.Tensor) or qw.dim() != 2:
+        raise TypeError("qw must be a 2-D CUDA tensor")
+    N = qw.shape[0]
+    _on(qw, torch.int8, "qw", (N, K), dev)
+    _on(sw, torch.float32, "sw", (N,), dev)
+    if bias is not None:
+        _on(bias, torch.float32, "bias", (N,), dev)
+    ldr = 0 if residual is None else _row_stride(residual, torch.bfloat16, "residual", dev, (M, N))
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    ldy = _row_stride(y, torch.bfloat16, "y", dev, (M, N))
+    if ws is None:
+        ws = _workspace(linear_workspace_size(M, N, K), dev)
+    _check(lib().w8a8_linear_epilogue(_ptr(x), ldx, _ptr(qw), _ptr(sw), _ptr(bias), act, _ptr(residual), ldr, _ptr(y),
+                                      ldy, M, N, K, _ptr(ws), ws.numel(), _stream()), "w8a8_linear_epilogue")
+    return y
+
+
+# ------------------------------------------------------------------ paged cache and attention
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale, device):
+    """(pages, Hkv, page size, D) of a paged cache: int8 with scales, or bf16 without."""
+    dtype = torch.bfloat16 if k_scale is None else torch.int8
+    _need(k_cache, dtype, "k_cache", 4)
+    shape = k_cache.shape
+    _on(k_cache, dtype, "k_cache", shape, device)
+    _on(v_cache, dtype, "v_cache", shape, device)
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale are given together or not at all")
+    if k_scale is not None:
+        _on(k_scale, torch.float32, "k_scale", shape[:3], device)
+        _on(v_scale, torch.float32, "v_scale", shape[:3], device)
+    return shape
+
+
+@_placed
+def kv_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None) -> None:
+    """Writes the keys and values of T tokens into the paged cache, in place.
+
+    k, v bf16 [T,Hkv,D] (token stride a multiple of 8, the rest dense); caches [pages,Hkv,page_size,D], int8 with
+    scales fp32 [pages,Hkv,page_size] or bf16 without; slots int64 [T], page * page_size + position, negative to
+    skip a token, distinct otherwise.  A slot past the cache is skipped and shows in get_device_error()."""
+    dev = k.device
+    ldk = _row_stride(k, torch.bfloat16, "k", dev, ndim=3)
+    ldv = _row_stride(v, torch.bfloat16, "v", dev, k.shape, ndim=3)
+    pages, Hkv, page, D = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
+    T = k.shape[0]
+    if k.shape[1:] != (Hkv, D):
+        raise ValueError(f"k has heads {tuple(k.shape[1:])}, the cache {(Hkv, D)}")
+    _on(slots, torch.int64, "slots", (T,), dev)
+    _check(lib().w8a8_kv_append(_ptr(k), ldk, _ptr(v), ldv, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                _ptr(slots), T, Hkv, D, pages, page, _stream()), "w8a8_kv_append")
+
+
+def paged_attention_workspace_size(B: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().w8a8_paged_attention_workspace_size(B, Hq, Hkv, D))
+
+
+@_placed
+def paged_attention(q, k_cache, v_cache, block_table, lengths, scale: float | None = None, k_scale=None, v_scale=None,
+                    y=None, ws=None) -> torch.Tensor:
+    """Attention of one new token per sequence over the paged cache -> bf16 [B,Hq,D].
+
+    q bf16 [B,Hq,D] (sequence stride a multiple of 8, the rest dense); caches as in :func:`kv_append`; block_table
+    int32 [B,max_pages], lengths int32 [B] (the new token included).  scale defaults to D ** -0.5.  A sequence of
+    length 0 gives zeros; absent pages and lengths past the table show in get_device_error()."""
+    dev = q.device
+    ldq = _row_stride(q, torch.bfloat16, "q", dev, ndim=3)
+    pages, Hkv, page, D = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
+    B, Hq, _ = q.shape
+    if q.shape[2] != D:
+        raise ValueError(f"q has head dim {q.shape[2]}, the cache {D}")
+    ld_table = _row_stride(block_table, torch.int32, "block_table", dev)
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must have a row per sequence")
+    _on(lengths, torch.int32, "lengths", (B,), dev)
+    if y is None:
+        y = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=dev)
+    _on(y, torch.bfloat16, "y", (B, Hq, D), dev)
+    if ws is None:
+        ws = _workspace(paged_attention_workspace_size(B, Hq, Hkv, D), dev)
+    _check(lib().w8a8_paged_attention(_ptr(q), ldq, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                      _ptr(block_table), ld_table, _ptr(lengths), _ptr(y), B, Hq, Hkv, D, pages, page,
+                                      block_table.shape[1], D ** -0.5 if scale is None else scale, _ptr(ws),
+                                      ws.numel(), _stream()), "w8a8_paged_attention")
+    return y
+
+
+# ------------------------------------------------------------------ log probabilities
+
+@_placed
+def token_logprobs(logits, tokens=None, topk: int = 0, entropy: bool = True):
+    """Log probabilities from the head's logits [M,V], bf16 or fp32 (rows may be strided).
+
+    Returns (logprob, entropy, top_ids, top_logprobs): fp32 of the shape of tokens (int32 [M] or [M,G]; NaN for a
+    token outside the vocabulary), fp32 [M] in nats, int32 [M,topk] by descending logit with ties to the lower index,
+    fp32 [M,topk].  None for what was not asked for."""
+    dev = logits.device
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
+    ld = _row_stride(logits, logits.dtype, "logits", dev)
+    M, V = logits.shape
+    G, logprob, ids, top = 0, None, None, None
+    if tokens is not None:
+        _need(tokens, torch.int32, "tokens")
+        if tokens.dim() not in (1, 2) or tokens.shape[0] != M:
+            raise ValueError("tokens must be [M] or [M, G]")
+        _on(tokens, torch.int32, "tokens", tokens.shape, dev)
+        G = 1 if tokens.dim() == 1 else tokens.shape[1]
+        logprob = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
+    h = torch.empty(M, dtype=torch.float32, device=dev) if entropy else None
+    if topk > 0:
+        ids = torch.empty((M, topk), dtype=torch.int32, device=dev)
+        top = torch.empty((M, topk), dtype=torch.float32, device=dev)
+    _check(lib().w8a8_token_logprobs(_ptr(logits), int(logits.dtype == torch.float32), ld, _ptr(tokens), G,
+                                     _ptr(logprob), _ptr(h), _ptr(ids), _ptr(top), M, V, topk, _stream()),
+           "w8a8_token_logprobs")
+    return logprob, h, ids, top
 
 
 # ------------------------------------------------------------------ diagnostics
