@@ -6,30 +6,36 @@
 //
 // Bound by the cache's bytes: each key and value is read once, by whichever
 // CTA holds its part of the context, for all the query heads that share it.
-// The arithmetic rides on warp MMAs (m16n8k16, fp32 sums) whose fragments are
-// the loaded registers themselves: no shared memory in the loop.
+// Every warp streams tiles of TT tokens of its own through a ring in shared
+// memory (cp.async, 16 bytes a lane, zeros in place of absent tokens), so that
+// one to two tiles a warp, 100 to 200 KB an SM, are in flight whatever the
+// arithmetic does.  The arithmetic rides on warp MMAs (fp32 or int32 sums):
 //
-//   lane = 4 g + c (g = 0..7, c = 0..3); a tile of TT tokens per warp step
-//   scores   S[query, token] = Q (16 x 16 over d) * K^T (16 d x 8 tokens):
-//     lane loads 16 contiguous bytes of token row 8j + g; which d a fragment
-//     slot means is free as long as Q's registers hold the same d's, so the
-//     16 bytes feed the B operand as they are (four steps of int8, two of bf16)
-//   outputs  O^T[d, query] = V^T (16 d x 16 tokens) * P^T (16 tokens x 8):
-//     the scores' accumulators (query g, tokens 8j + 2c, + 1) are the B
-//     operand's layout already; lane loads 16 contiguous bytes of d from each
-//     of its tokens and pairs them across tokens with byte permutes
+//   lane = 4 g + c (g = 0..7, c = 0..3)
+//   scores   S[query, token] = Q * K^T: lane takes 16 contiguous bytes of
+//     token row 8j + g; which d a fragment slot means is free as long as Q's
+//     hold the same d's, so the 16 bytes are the B operand as they are
+//   outputs  O^T[d, query] = V^T (16 d x 16 tokens) * P^T (16 tokens x 8): the
+//     scores' accumulators (query g, tokens 8j + 2c, + 1) have the B operand's
+//     layout already; lane takes 16 contiguous bytes of d from each of its
+//     tokens and pairs them across tokens with byte permutes
 //
-// int8 codes become fp16 exactly: the bytes, offset to unsigned, are placed
-// under the exponent of 1024 (1024 + u), less 1152.  The query is scaled per
-// head by a power of two to fp16 (8 significant bits fit 11: exact but for
-// elements 2^-15 below the largest); the scales of keys multiply the scores,
-// those of values the probabilities, which are then brought to [0, 2) by a
-// running power of two per query before they round to fp16 (2^-12, an eighth
-// of the output's own rounding).  With a bf16 cache the probabilities go in as
-// the sum of two bf16 (2^-17).
+// int8 cache.  Scores are int8 MMAs on the codes themselves: the query's head
+// is scaled by a power of two to 21-bit integers and cut into three planes of
+// signed 7 bits (exact but for elements 2^-12 below its largest, which round
+// to 2^-20 of it); with up to 8 query heads the first two planes are the upper
+// and lower half of one MMA's 16 rows.  The int32 sums are exact and join in
+// fp32.  Keys' scales multiply the scores, values' scales the probabilities,
+// which a running power of two per query brings to [0, 2) before they round
+// to fp16 (2^-11, an eighth of the output's own rounding); the values' codes
+// become fp16 exactly (the byte, offset to unsigned, under the exponent of
+// 1024, less 1152).  bf16 cache: bf16 MMAs, with the probabilities as the sum
+// of two bf16 (2^-16).
 //
 // Work split: chunks of 4 tiles (one per warp), ordered by (sequence, head),
-// in equal contiguous shares over a fixed grid, whatever the lengths are.  A
+// in equal contiguous shares over a fixed grid, whatever the lengths are (a
+// share is ceil(chunks / grid): the largest of any even split, and who holds a
+// chunk is one division).  A
 // CTA's share is cut where a (sequence, head) ends; one that it holds whole is
 // written out, of one it shares it leaves (m, sum p, sum p v) in fp32 for
 // attn_join_kernel, which adds the parts in order.
@@ -139,19 +145,19 @@ __device__ __forceinline__ int64_t attn_len(const AttnArgs& a, int b) {
     return n < 0 ? 0 : (n > a.cap ? a.cap : n);
 }
 
-// Sequence that holds unit u0 of (sum over b of chunks(b)) * heads units, the
-// chunks before it, and the units in all.  All threads of the CTA call it.
+// CTA's share [u0, u1) of the (sum over b of chunks(b)) * heads units, the
+// sequence that holds u0 and the chunks before it.  All threads call it.
 struct AttnPlace {
     int b;
-    int64_t before, total;
+    int64_t before, u0, u1;   // the CTA's units
 };
 template <int CH, int NT>
-__device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a, int grid, int cta, int64_t heads) {
+__device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a, int cta, int64_t heads) {
     __shared__ int64_t wsum[NT / 32];
     __shared__ AttnPlace place;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (a.B + NT - 1) / NT;
-    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    const int seqs = (a.B + NT - 1) / NT;   // a thread's
+    const int b0 = min(tid * seqs, a.B), b1 = min(b0 + seqs, a.B);
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) mine += (attn_len(a, b) + CH - 1) / CH;
     int64_t inc = mine;
@@ -169,7 +175,8 @@ __device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a, int grid, int
         total += wsum[w];
     }
     total *= heads;
-    const int64_t u0 = total * cta / grid;
+    const int64_t per = (total + a.grid - 1) / a.grid;
+    const int64_t u0 = per * cta < total ? per * cta : total;
     if (u0 >= before * heads && u0 < (before + mine) * heads) {
         int b = b0;
         for (; b < b1 - 1; ++b) {
@@ -180,7 +187,10 @@ __device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a, int grid, int
         place.b = b;
         place.before = before;
     }
-    if (tid == 0) place.total = total;
+    if (tid == 0) {
+        place.u0 = u0;
+        place.u1 = u0 + per < total ? u0 + per : total;
+    }
     __syncthreads();
     return place;
 }
@@ -216,32 +226,76 @@ __device__ __forceinline__ float attn_ex2(float x) {
     return y;
 }
 
-// NQ: tiles of 8 query heads a pass (QT = 8 NQ of the heads that share a key-value head).
-template <int D, bool INT8, int NQ, int MINB>
-__global__ void __launch_bounds__(kAttnThreads, MINB) paged_attention_kernel(AttnArgs a) {
-    constexpr int TT = attn_tt<D, INT8>();
-    constexpr int CH = kAttnWarps * TT;
-    constexpr int QT = 8 * NQ;
-    constexpr int ROW = INT8 ? D : 2 * D;             // bytes of a cache row
+// 16 bytes to shared memory, the first `bytes` of them from global memory, zeros behind.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+
+// Sizes of one instance.  NQ: tiles of 8 query heads a pass.
+template <int D, bool INT8, int NQ>
+struct AttnCfg {
+    static constexpr int TT = attn_tt<D, INT8>();
+    static constexpr int CH = kAttnWarps * TT;
+    static constexpr int QT = 8 * NQ;
+    static constexpr int ROW = INT8 ? D : 2 * D;             // bytes of a cache row
+    static constexpr int U = ROW / 16;                       // 16-byte units of a row
+    static constexpr int kScales = INT8 ? TT * 4 : 0;
+    static constexpr int kStage = 2 * (TT * ROW + kScales);  // keys, values, their scales
+    static constexpr int kStages = kStage <= 4608 ? 4 : 2;
+    static constexpr int kRing = kStages * kStage;           // a warp's
+    // words of Q's fragments per lane and MMA k step: three planes of int8, or bf16
+    static constexpr int kQWords = INT8 ? (NQ == 1 ? 6 : 12) : 2 * NQ;
+    static constexpr int kQSteps = INT8 ? D / 32 : D / 16;
+    static constexpr int kQ = kQSteps * 32 * kQWords * 4;
+    static constexpr int kJoin = kAttnWarps * QT * (D + 4) * 4;   // over the ring, between segments
+    static constexpr int kBytes = kQ + (kAttnWarps * kRing > kJoin ? kAttnWarps * kRing : kJoin);
+    static constexpr int kMinB = (227 * 1024) / (kBytes + 2048) >= 3 && !(NQ == 2 && D == 256) ? 3
+                               : (227 * 1024) / (kBytes + 2048) >= 2                           ? 2
+                                                                                               : 1;
+};
+
+template <int D, bool INT8, int NQ>
+__global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) paged_attention_kernel(AttnArgs a) {
+    using Cfg = AttnCfg<D, INT8, NQ>;
+    constexpr int TT = Cfg::TT, CH = Cfg::CH, QT = Cfg::QT, ROW = Cfg::ROW, U = Cfg::U, ST = Cfg::kStages;
     constexpr int KL = ROW / 64;                      // 16-byte key loads per token and lane
-    constexpr int KS = INT8 ? 4 : 2;                  // k steps of 16 per load
     constexpr int NT8 = TT / 8;                       // score tiles of 8 tokens
-    constexpr int VB = D * (INT8 ? 1 : 2) / 8 < 16 ? 8 : 16;   // bytes per value load (8 for int8 rows of 64)
+    constexpr int VB = U == 4 ? 8 : 16;               // bytes per value load
     constexpr int VL = ROW / (8 * VB);                // value loads per token and lane
     constexpr int VW = VB / 4;                        // words per value load
     constexpr int OT = D / 16;                        // output tiles of 16 d
     constexpr int DPL = INT8 ? VB : VB / 2;           // d's per value load and lane
+    constexpr int QW = Cfg::kQWords;
 
-    __shared__ __align__(16) float so[kAttnWarps][QT][D + 4];
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float sm[kAttnWarps][QT], sl[kAttnWarps][QT];
+    uint32_t* qs = reinterpret_cast<uint32_t*>(smem);         // Q's fragments: [step][word / 2][lane][2]
+    float* so = reinterpret_cast<float*>(smem + Cfg::kQ);     // [warp][QT][D + 4], between segments
 
     // attn_join_kernel may launch; it waits for this grid before it reads the parts
     asm volatile("griddepcontrol.launch_dependents;");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const uint32_t ring = smem_u32(smem) + Cfg::kQ + warp * Cfg::kRing;
+    const uint32_t qbase = smem_u32(smem) + lane * 8;
     const int64_t heads = (int64_t)a.Hkv * a.qtiles;
-    const AttnPlace place = attn_place<CH, kAttnThreads>(a, a.grid, blockIdx.x, heads);
-    int64_t u = place.total * blockIdx.x / a.grid;
-    const int64_t u1 = place.total * (blockIdx.x + 1) / a.grid;
+    const AttnPlace place = attn_place<CH, kAttnThreads>(a, blockIdx.x, heads);
+    int64_t u = place.u0;
+    const int64_t u1 = place.u1;
     int b = place.b;
     int64_t before = place.before;
     const int pmask = (1 << a.page_shift) - 1;
@@ -261,61 +315,144 @@ __global__ void __launch_bounds__(kAttnThreads, MINB) paged_attention_kernel(Att
         const int64_t seg = nb - ch0 < u1 - u ? nb - ch0 : u1 - u;
         const int h = hq / a.qtiles, qt = hq - h * a.qtiles;
         const int nq = min(QT, a.G - qt * QT);        // query heads of this tile
+        const int q0 = h * a.G + qt * QT;             // the first of them
 
-        // ---- the query's fragments
-        uint32_t qf[KL * KS][NQ][2];
+        // ---- the warp's tiles: ch0 * 4 + warp, every fourth
+        const int64_t tile_end = (ch0 + seg) * kAttnWarps;
+        const int32_t* trow = a.table + (int64_t)b * a.ld_table;
+        auto page_of = [&](int64_t tile) -> int {     // of the tile's token number `lane`; < 0: absent
+            const int64_t t = tile * TT + lane;
+            if (tile >= tile_end || lane >= TT || t >= len) return -1;
+            const int pg = __ldg(trow + (t >> a.page_shift));
+            if (pg < 0 || pg >= a.num_pages) {
+                bad = true;
+                return -1;
+            }
+            return pg;
+        };
+        // Copies a tile: eight tokens at a time lie in one page, their rows one
+        // after the other.  In shared memory a key row's units are XORed with 4
+        // on odd rows and a value row's with 2 * (row / 2 % 4), which keeps both
+        // reads below (8 rows x 4 units; 4 even or odd rows x 2 units) free of
+        // bank conflicts.
+        auto issue = [&](int pages, int64_t tile, int stage) {
+            const uint32_t ks = ring + stage * Cfg::kStage, vs = ks + TT * ROW, cs = vs + TT * ROW;
+            int64_t row0[NT8];
+            int here[NT8];
+#pragma unroll
+            for (int j = 0; j < NT8; ++j) {
+                const int pg = __shfl_sync(0xffffffffu, pages, 8 * j);
+                const int64_t t = tile * TT + 8 * j;
+                here[j] = pg < 0 ? 0 : (int)(len - t < 8 ? len - t : 8);
+                row0[j] = pg < 0 ? 0 : (((int64_t)pg * a.Hkv + h) << a.page_shift) + ((int)t & pmask);
+                const uint8_t* ksrc = reinterpret_cast<const uint8_t*>(a.kc) + row0[j] * ROW + 16 * lane;
+                const uint8_t* vsrc = reinterpret_cast<const uint8_t*>(a.vc) + row0[j] * ROW + 16 * lane;
+#pragma unroll
+                for (int x = 0; x < U / 4; ++x) {
+                    const int r = (x * 32 + lane) / U, un = (x * 32 + lane) % U;
+                    const uint32_t n = r < here[j] ? 16u : 0u;
+                    const int ku = U == 4 ? un : un ^ ((r & 1) << 2), vu = U == 4 ? un : un ^ (((r >> 1) & 3) << 1);
+                    cp_async16(ks + ((8 * j + r) * U + ku) * 16, ksrc + 512 * x, n);
+                    cp_async16(vs + ((8 * j + r) * U + vu) * 16, vsrc + 512 * x, n);
+                }
+            }
+            if (INT8 && lane < 4 * NT8) {
+                // lanes [0, 2 NT8): keys' scales, four tokens each; then values'
+                const int j = (lane >> 1) % NT8, half = lane & 1;
+                int64_t row = row0[0];
+                int n = here[0];
+#pragma unroll
+                for (int i = 1; i < NT8; ++i)
+                    if (j == i) {
+                        row = row0[i];
+                        n = here[i];
+                    }
+                const int left = min(max(n - 4 * half, 0), 4);
+                cp_async16(cs + lane * 16, (lane < 2 * NT8 ? a.ks : a.vs) + row + 4 * half, 4u * left);
+            }
+        };
+        int64_t tile = ch0 * kAttnWarps + warp;
+#pragma unroll
+        for (int s = 0; s < ST; ++s) {
+            issue(page_of(tile + s * kAttnWarps), tile + s * kAttnWarps, s);
+            cp_async_commit();
+        }
+        int pages_next = page_of(tile + ST * kAttnWarps);
+
+        // ---- the query's fragments, a share of the k steps per warp
         float qscale[NQ];
-        const int q0 = h * a.G + qt * QT;             // first query head
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             qscale[n] = a.scale_log2;
             const bool has = 8 * n + g < nq;
             const uint16_t* qrow = a.q + (int64_t)b * a.ldq + (int64_t)(q0 + 8 * n + g) * D;
             if (INT8) {
-                // 16 d's per load and lane: d = 64 j + 16 c + e
+                // 16 d's per key load and lane: d = 64 i + 16 c + e
                 float amax = 0.0f;
+                uint4 w[KL][2];
 #pragma unroll
-                for (int j = 0; j < KL; ++j) {
-                    uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                    if (has) {
-                        w[0] = __ldg(reinterpret_cast<const uint4*>(qrow + 64 * j + 16 * c));
-                        w[1] = __ldg(reinterpret_cast<const uint4*>(qrow + 64 * j + 16 * c + 8));
+                for (int i = 0; i < KL; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        w[i][e] = make_uint4(0, 0, 0, 0);
+                        if (has) w[i][e] = __ldg(reinterpret_cast<const uint4*>(qrow + 64 * i + 16 * c + 8 * e));
+                        const uint32_t x[4] = {w[i][e].x, w[i][e].y, w[i][e].z, w[i][e].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            amax = fmax_nan(amax, fmax_nan(fabsf(__uint_as_float(x[k] << 16)),
+                                                           fabsf(__uint_as_float(x[k] & 0xffff0000u))));
                     }
-                    const uint32_t x[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+                amax = fmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                // amax in [2^e, 2^(e+1)): integers q 2^(19-e), below 2^20; NaN and infinities pass through the scale
+                const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100);
+                const float up = __uint_as_float((uint32_t)(min(19 - e, 127) + 127) << 23);
+                qscale[n] *= amax < INFINITY ? __uint_as_float((uint32_t)(e - 19 + 127) << 23) : __int_as_float(0x7fc00000);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        qf[j * KS + i / 2][n][i & 1] = x[i];
-                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[i] << 16)),
-                                                 fabsf(__uint_as_float(x[i] & 0xffff0000u))));
+                for (int i = 0; i < KL; ++i) {
+                    if (i % kAttnWarps != warp) continue;
+#pragma unroll
+                    for (int st = 0; st < 2; ++st) {         // MMA step 2 i + st: d = 64 i + 16 c + 8 st + [0, 8)
+                        const uint32_t x[4] = {w[i][st].x, w[i][st].y, w[i][st].z, w[i][st].w};
+                        int p[3][8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float f = __uint_as_float(k & 1 ? x[k / 2] & 0xffff0000u : x[k / 2] << 16);
+                            const int v = __float2int_rn(f * up);
+                            p[0][k] = (v + 8192) >> 14;
+                            const int r = v - (p[0][k] << 14);
+                            p[1][k] = (r + 64) >> 7;
+                            p[2][k] = r - (p[1][k] << 7);
+                        }
+#pragma unroll
+                        for (int pl = 0; pl < 3; ++pl)
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                const uint32_t v = pack4_s8(p[pl][4 * hf], p[pl][4 * hf + 1], p[pl][4 * hf + 2], p[pl][4 * hf + 3]);
+                                // NQ = 1: words (a0, a1, a2, a3) = planes 0, 1, 0, 1; then plane 2.
+                                // NQ = 2: plane by plane (a0, a1, a2, a3)
+                                const int word = NQ == 1 ? (pl < 2 ? 2 * hf + pl : 4 + hf) : 4 * pl + 2 * hf + n;
+                                qs[(((2 * i + st) * (QW / 2) + word / 2) * 32 + lane) * 2 + (word & 1)] = v;
+                            }
                     }
                 }
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                // 2^e with amax * 2^-e in [1, 2)
-                const int ex = min(max((int)(__float_as_uint(amax) >> 23), 1), 253);
-                const float down = __uint_as_float((uint32_t)(254 - ex) << 23), up = __uint_as_float((uint32_t)ex << 23);
-                qscale[n] *= up;
-#pragma unroll
-                for (int i = 0; i < KL * KS; ++i)
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const uint32_t x = qf[i][n][w];
-                        const __half2 hv = __floats2half2_rn(__uint_as_float(x << 16) * down,
-                                                             __uint_as_float(x & 0xffff0000u) * down);
-                        qf[i][n][w] = *reinterpret_cast<const uint32_t*>(&hv);
-                    }
             } else {
+                // 8 d's per key load and lane: d = 32 i + 8 c + e; words (a0, a2), or (a0, a1, a2, a3) of two tiles
 #pragma unroll
-                for (int j = 0; j < KL; ++j) {
+                for (int i = 0; i < KL; ++i) {
+                    if (i % kAttnWarps != warp) continue;
                     uint4 w = make_uint4(0, 0, 0, 0);
-                    if (has) w = __ldg(reinterpret_cast<const uint4*>(qrow + 32 * j + 8 * c));
-                    qf[2 * j][n][0] = w.x;
-                    qf[2 * j][n][1] = w.y;
-                    qf[2 * j + 1][n][0] = w.z;
-                    qf[2 * j + 1][n][1] = w.w;
+                    if (has) w = __ldg(reinterpret_cast<const uint4*>(qrow + 32 * i + 8 * c));
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int word = (k & 1) * NQ + n;
+                        qs[(((2 * i + k / 2) * (QW / 2) + word / 2) * 32 + lane) * 2 + (word & 1)] = x[k];
+                    }
                 }
             }
         }
+        __syncthreads();
 
         float o[NQ][OT][4];
         float m[NQ], l[NQ];
@@ -331,104 +468,116 @@ __global__ void __launch_bounds__(kAttnThreads, MINB) paged_attention_kernel(Att
                 for (int j = 0; j < 4; ++j) o[n][i][j] = 0.0f;
         }
 
-        // ---- the warp's tiles: ch0 * 4 + warp, every fourth
-        const int64_t tile_end = (ch0 + seg) * kAttnWarps;
-        const int32_t* trow = a.table + (int64_t)b * a.ld_table;
-        auto page_of = [&](int64_t tile) -> int {     // of the tile's token number `lane`
-            const int64_t t = tile * TT + lane;
-            if (tile >= tile_end || lane >= TT || t >= len) return -1;
-            const int pg = __ldg(trow + (t >> a.page_shift));
-            if (pg < 0 || pg >= a.num_pages) {
-                bad = true;
-                return -1;
-            }
-            return pg;
-        };
-        // row of token x of a tile whose tokens' pages the lanes hold; < 0: absent
-        auto row_of = [&](int pages, int64_t tile, int x) -> int64_t {
-            const int pg = __shfl_sync(0xffffffffu, pages, x);
-            const int off = (int)((tile * TT + x) & pmask);
-            return pg < 0 ? -1 : ((((int64_t)pg * a.Hkv + h) << a.page_shift) + off);
-        };
-        uint4 kr[NT8][KL];
-        uint32_t vr[NT8][2][VL][VW];                  // tokens 8j + 2c, 8j + 2c + 1
-        float2 ksc[NT8], vsc[NT8];
-        auto load_k = [&](int pages, int64_t tile) {
-#pragma unroll
-            for (int j = 0; j < NT8; ++j) {
-                const int64_t row = row_of(pages, tile, 8 * j + g);
-                const uint8_t* p = reinterpret_cast<const uint8_t*>(a.kc) + row * ROW + 16 * c;
-#pragma unroll
-                for (int i = 0; i < KL; ++i) kr[j][i] = row >= 0 ? ld_stream_16(p + 64 * i) : make_uint4(0, 0, 0, 0);
-            }
-        };
-        auto load_v = [&](int pages, int64_t tile) {
-#pragma unroll
-            for (int j = 0; j < NT8; ++j) {
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int64_t row = row_of(pages, tile, 8 * j + 2 * c + s);
-                    const uint8_t* p = reinterpret_cast<const uint8_t*>(a.vc) + row * ROW + VB * g;
-#pragma unroll
-                    for (int i = 0; i < VL; ++i) {
-                        if (VB == 16) {
-                            const uint4 v = row >= 0 ? ld_stream_16(p + 128 * i) : make_uint4(0, 0, 0, 0);
-                            vr[j][s][i][0] = v.x;
-                            vr[j][s][i][1] = v.y;
-                            vr[j][s][i][2 % VW] = v.z;
-                            vr[j][s][i][3 % VW] = v.w;
-                        } else {
-                            const uint2 v = row >= 0 ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
-                            vr[j][s][i][0] = v.x;
-                            vr[j][s][i][1] = v.y;
-                        }
-                    }
-                    if (INT8) {
-                        const float sk = row >= 0 ? __ldg(a.ks + row) : 0.0f, sv = row >= 0 ? __ldg(a.vs + row) : 0.0f;
-                        if (s == 0) {
-                            ksc[j].x = sk;
-                            vsc[j].x = sv;
-                        } else {
-                            ksc[j].y = sk;
-                            vsc[j].y = sv;
-                        }
-                    }
-                }
-            }
-        };
-
-        int64_t tile = ch0 * kAttnWarps + warp;
-        int pages = page_of(tile), pages_next = page_of(tile + kAttnWarps);
-        load_k(pages, tile);
-        load_v(pages, tile);
+        int stage = 0;
         for (; tile < tile_end; tile += kAttnWarps) {
-            const uint32_t valid = __ballot_sync(0xffffffffu, pages >= 0);
+            cp_async_wait<ST - 1>();
+            __syncwarp();
+            const uint32_t ks = ring + stage * Cfg::kStage, vs = ks + TT * ROW, cs = vs + TT * ROW;
             // ---- scores
-            float s[NT8][4];
+            float s[NQ][NT8][2];
+            if (INT8) {
+                int hi[NQ][NT8][4], lo[NQ][NT8][4], mid[NQ == 2 ? NT8 : 1][4];
 #pragma unroll
-            for (int j = 0; j < NT8; ++j) {
+                for (int j = 0; j < NT8; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[j][i] = 0.0f;
+                    for (int k = 0; k < 4; ++k) {
+                        hi[0][j][k] = lo[0][j][k] = 0;
+                        if (NQ == 2) mid[j % (NQ == 2 ? NT8 : 1)][k] = 0;
+                    }
 #pragma unroll
                 for (int i = 0; i < KL; ++i) {
-                    const uint32_t w[4] = {kr[j][i].x, kr[j][i].y, kr[j][i].z, kr[j][i].w};
+                    uint4 kr[NT8];
 #pragma unroll
-                    for (int st = 0; st < KS; ++st) {
-                        const uint32_t(&qa)[NQ][2] = qf[i * KS + st];
-                        const uint32_t a1 = NQ == 2 ? qa[NQ - 1][0] : 0u, a3 = NQ == 2 ? qa[NQ - 1][1] : 0u;
-                        if (INT8) {
-                            const uint32_t u8 = w[st] ^ 0x80808080u;
-                            mma_f16_16816(s[j], qa[0][0], a1, qa[0][1], a3, code_pair<0x4140>(u8), code_pair<0x4342>(u8));
-                        } else {
-                            mma_bf16_16816(s[j], qa[0][0], a1, qa[0][1], a3, w[(2 * st) % 4], w[(2 * st + 1) % 4]);
+                    for (int j = 0; j < NT8; ++j)
+                        kr[j] = lds16(ks + ((8 * j + g) * U + (U == 4 ? c : (4 * i + c) ^ ((g & 1) << 2))) * 16);
+#pragma unroll
+                    for (int st = 0; st < 2; ++st) {
+                        uint32_t q[QW];
+#pragma unroll
+                        for (int w = 0; w < QW / 2; ++w) {
+                            const uint2 v = lds8(qbase + ((2 * i + st) * (QW / 2) + w) * 256);
+                            q[2 * w] = v.x;
+                            q[2 * w + 1] = v.y;
+                        }
+#pragma unroll
+                        for (int j = 0; j < NT8; ++j) {
+                            const uint32_t bk[2] = {st ? kr[j].z : kr[j].x, st ? kr[j].w : kr[j].y};
+                            const uint32_t a0[4] = {q[0], q[1], q[2], q[3]};
+                            mma_s8_16832(hi[0][j], a0, bk);
+                            if (NQ == 1) {
+                                const uint32_t a1[4] = {q[4], 0u, q[5], 0u};
+                                mma_s8_16832(lo[0][j], a1, bk);
+                            } else {
+                                const uint32_t a1[4] = {q[4 % QW], q[5 % QW], q[6 % QW], q[7 % QW]};
+                                const uint32_t a2[4] = {q[8 % QW], q[9 % QW], q[10 % QW], q[11 % QW]};
+                                mma_s8_16832(mid[j % (NQ == 2 ? NT8 : 1)], a1, bk);
+                                mma_s8_16832(lo[0][j], a2, bk);
+                            }
                         }
                     }
                 }
+                // planes join: |sums| < 2^22, exact in fp32
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int j = 0; j < NT8; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int p0 = hi[0][j][2 * n + e];
+                            const int p1 = NQ == 1 ? hi[0][j][2 + e] : mid[j % (NQ == 2 ? NT8 : 1)][2 * n + e];
+                            const int p2 = lo[0][j][2 * n + e];
+                            s[n][j][e] = __fmaf_rn(16384.0f, __int2float_rn(p0),
+                                                   __fmaf_rn(128.0f, __int2float_rn(p1), __int2float_rn(p2)));
+                        }
+            } else {
+                float acc[NT8][4];
+#pragma unroll
+                for (int j = 0; j < NT8; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[j][k] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < KL; ++i) {
+                    uint4 kr[NT8];
+#pragma unroll
+                    for (int j = 0; j < NT8; ++j) kr[j] = lds16(ks + ((8 * j + g) * U + ((4 * i + c) ^ ((g & 1) << 2))) * 16);
+#pragma unroll
+                    for (int st = 0; st < 2; ++st) {
+                        uint32_t q[QW];
+#pragma unroll
+                        for (int w = 0; w < QW / 2; ++w) {
+                            const uint2 v = lds8(qbase + ((2 * i + st) * (QW / 2) + w) * 256);
+                            q[2 * w] = v.x;
+                            q[2 * w + 1] = v.y;
+                        }
+#pragma unroll
+                        for (int j = 0; j < NT8; ++j)
+                            mma_bf16_16816(acc[j], q[0], NQ == 2 ? q[1] : 0u, NQ == 2 ? q[2 % QW] : q[1],
+                                           NQ == 2 ? q[3 % QW] : 0u, st ? kr[j].z : kr[j].x, st ? kr[j].w : kr[j].y);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int j = 0; j < NT8; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) s[n][j][e] = acc[j][2 * n + e];
             }
-            const int64_t next = tile + kAttnWarps;
-            load_k(pages_next, next);   // in flight during the softmax and the outputs
-            const int pages_after = page_of(next + kAttnWarps);
             // ---- softmax of query rows g (and g + 8)
+            const int64_t left = len - tile * TT;     // tokens from here on
+            uint32_t there = 0xffffffffu;             // bit t: token t is there
+            if (left < TT || __any_sync(0xffffffffu, lane < TT && bad)) {
+                const int pg = page_of(tile);
+                there = __ballot_sync(0xffffffffu, pg >= 0);
+            }
+            float2 ksc[NT8], vsc[NT8];
+            if (INT8) {
+#pragma unroll
+                for (int j = 0; j < NT8; ++j) {
+                    const uint2 kx = lds8(cs + (8 * j + 2 * c) * 4), vx = lds8(cs + TT * 4 + (8 * j + 2 * c) * 4);
+                    ksc[j] = make_float2(__uint_as_float(kx.x), __uint_as_float(kx.y));
+                    vsc[j] = make_float2(__uint_as_float(vx.x), __uint_as_float(vx.y));
+                }
+            }
             uint32_t pf[NQ][NT8], pl[NQ][NT8];        // fp16 pairs; bf16: high and low parts
             float fac[NQ];
             bool rescale = false;
@@ -440,9 +589,9 @@ __global__ void __launch_bounds__(kAttnThreads, MINB) paged_attention_kernel(Att
                 for (int j = 0; j < NT8; ++j) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float v = s[j][2 * n + e] * qscale[n];
+                        float v = s[n][j][e] * qscale[n];
                         if (INT8) v *= e ? ksc[j].y : ksc[j].x;
-                        x[j][e] = (valid >> (8 * j + 2 * c + e)) & 1u ? v : -INFINITY;
+                        x[j][e] = (there >> (8 * j + 2 * c + e)) & 1u ? v : -INFINITY;
                         mx = fmaxf(mx, x[j][e]);
                     }
                 }
@@ -472,8 +621,8 @@ __global__ void __launch_bounds__(kAttnThreads, MINB) paged_attention_kernel(Att
                     }
                     um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 1));
                     um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 2));
-                    // largest so far in the new reference: the old unit's 2 * 2^oe * corr bounds the old ones
-                    const float old = __uint_as_float((uint32_t)min(max(oe[n] + 127, 0), 254) << 23) * corr;
+                    // the unit never falls below the old one's place in the new reference, so fac stays below 2
+                    const float old = __uint_as_float((uint32_t)(oe[n] + 127) << 23) * corr;
                     const int en = min(max((int)(__float_as_uint(fmaxf(um, old)) >> 23) - 127, -126), 126);
                     fac[n] = corr * __uint_as_float((uint32_t)min(max(oe[n] - en + 127, 0), 254) << 23);
                     oe[n] = en;
@@ -487,10 +636,10 @@ __global__ void __launch_bounds__(kAttnThreads, MINB) paged_attention_kernel(Att
                     fac[n] = corr;
 #pragma unroll
                     for (int j = 0; j < NT8; ++j) {
-                        const uint32_t hi = pack_bf16x2(x[j][0], x[j][1]);
+                        const uint32_t hi = cvt_bf16x2(x[j][0], x[j][1]);
                         pf[n][j] = hi;
-                        pl[n][j] = pack_bf16x2(x[j][0] - __uint_as_float(hi << 16),
-                                               x[j][1] - __uint_as_float(hi & 0xffff0000u));
+                        pl[n][j] = cvt_bf16x2(x[j][0] - __uint_as_float(hi << 16),
+                                              x[j][1] - __uint_as_float(hi & 0xffff0000u));
                     }
                 }
                 rescale |= fac[n] != 1.0f;
@@ -513,12 +662,28 @@ __global__ void __launch_bounds__(kAttnThreads, MINB) paged_attention_kernel(Att
             for (int j = 0; j < NT8; j += 2) {
 #pragma unroll
                 for (int i = 0; i < VL; ++i) {
+                    uint32_t vr[4][VW];               // tokens 8j + 2c, + 1, 8j + 8 + 2c, + 1
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const int r = 8 * (j + t / 2) + 2 * c + (t & 1);
+                        if (VB == 16) {
+                            const uint4 v = lds16(vs + (r * U + ((g + 8 * i) ^ (c << 1))) * 16);
+                            vr[t][0] = v.x;
+                            vr[t][1] = v.y;
+                            vr[t][2 % VW] = v.z;
+                            vr[t][3 % VW] = v.w;
+                        } else {
+                            const uint2 v = lds8(vs + r * ROW + 8 * g);
+                            vr[t][0] = v.x;
+                            vr[t][1] = v.y;
+                        }
+                    }
 #pragma unroll
                     for (int w = 0; w < VW; ++w) {
                         if (INT8) {
                             // 4 d's: two output tiles
-                            const uint32_t t0 = vr[j][0][i][w] ^ 0x80808080u, t1 = vr[j][1][i][w] ^ 0x80808080u;
-                            const uint32_t t2 = vr[j + 1][0][i][w] ^ 0x80808080u, t3 = vr[j + 1][1][i][w] ^ 0x80808080u;
+                            const uint32_t t0 = vr[0][w] ^ 0x80808080u, t1 = vr[1][w] ^ 0x80808080u;
+                            const uint32_t t2 = vr[2][w] ^ 0x80808080u, t3 = vr[3][w] ^ 0x80808080u;
                             const uint32_t x0 = __byte_perm(t0, t1, 0x5140), x1 = __byte_perm(t0, t1, 0x7362);
                             const uint32_t y0 = __byte_perm(t2, t3, 0x5140), y1 = __byte_perm(t2, t3, 0x7362);
                             const uint32_t a0 = code_pair<0x4140>(x0), a1 = code_pair<0x4342>(x0);
@@ -531,10 +696,10 @@ __global__ void __launch_bounds__(kAttnThreads, MINB) paged_attention_kernel(Att
                                 mma_f16_16816(o[n][(i * VW + w) * 2 + 1], b0, b1, b2, b3, pf[n][j], pf[n][j + 1]);
                             }
                         } else {
-                            const uint32_t a0 = __byte_perm(vr[j][0][i][w], vr[j][1][i][w], 0x5410);
-                            const uint32_t a1 = __byte_perm(vr[j][0][i][w], vr[j][1][i][w], 0x7632);
-                            const uint32_t a2 = __byte_perm(vr[j + 1][0][i][w], vr[j + 1][1][i][w], 0x5410);
-                            const uint32_t a3 = __byte_perm(vr[j + 1][0][i][w], vr[j + 1][1][i][w], 0x7632);
+                            const uint32_t a0 = __byte_perm(vr[0][w], vr[1][w], 0x5410);
+                            const uint32_t a1 = __byte_perm(vr[0][w], vr[1][w], 0x7632);
+                            const uint32_t a2 = __byte_perm(vr[2][w], vr[3][w], 0x5410);
+                            const uint32_t a3 = __byte_perm(vr[2][w], vr[3][w], 0x7632);
 #pragma unroll
                             for (int n = 0; n < NQ; ++n) {
                                 mma_bf16_16816(o[n][i * VW + w], a0, a1, a2, a3, pf[n][j], pf[n][j + 1]);
@@ -544,13 +709,17 @@ __global__ void __launch_bounds__(kAttnThreads, MINB) paged_attention_kernel(Att
                     }
                 }
             }
-            load_v(pages_next, next);   // in flight during the next scores
-            pages = pages_next;
-            pages_next = pages_after;
+            __syncwarp();   // the stage has been read
+            const int64_t next = tile + ST * kAttnWarps;
+            issue(pages_next, next, stage);
+            cp_async_commit();
+            pages_next = page_of(next + kAttnWarps);
+            stage = stage + 1 == ST ? 0 : stage + 1;
         }
 
-        // ---- join of the four warps
-        __syncthreads();   // the previous segment's reads are done
+        // ---- join of the four warps, over the rings (whose copies have all landed)
+        cp_async_wait<0>();
+        __syncthreads();
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
@@ -560,15 +729,16 @@ __global__ void __launch_bounds__(kAttnThreads, MINB) paged_attention_kernel(Att
                 sl[warp][8 * n + g] = l[n];
             }
             float un = 1.0f;
-            if (INT8) un = __uint_as_float((uint32_t)(min(max(oe[n], -126), 126) + 127) << 23);
+            if (INT8) un = __uint_as_float((uint32_t)(max(oe[n], -126) + 127) << 23);
             const float u0f = __shfl_sync(0xffffffffu, un, 8 * c), u1f = __shfl_sync(0xffffffffu, un, 8 * c + 4);
             // tile i covers d = 8 DPL (i / (DPL / 2)) + DPL g + 2 (i % (DPL / 2)), + 1
+            float* dst = so + (warp * QT + 8 * n + 2 * c) * (D + 4);
 #pragma unroll
             for (int i = 0; i < OT; i += 2) {
                 const int d = 8 * DPL * (i / (DPL / 2)) + DPL * g + 2 * (i % (DPL / 2));
-                *reinterpret_cast<float4*>(&so[warp][8 * n + 2 * c][d]) =
+                *reinterpret_cast<float4*>(dst + d) =
                     make_float4(o[n][i][0] * u0f, o[n][i][2] * u0f, o[n][i + 1][0] * u0f, o[n][i + 1][2] * u0f);
-                *reinterpret_cast<float4*>(&so[warp][8 * n + 2 * c + 1][d]) =
+                *reinterpret_cast<float4*>(dst + D + 4 + d) =
                     make_float4(o[n][i][1] * u1f, o[n][i][3] * u1f, o[n][i + 1][1] * u1f, o[n][i + 1][3] * u1f);
             }
         }
@@ -587,7 +757,7 @@ __global__ void __launch_bounds__(kAttnThreads, MINB) paged_attention_kernel(Att
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) {
                 const float f = attn_ex2(sm[w][qh] - mu);
-                const float4 v = *reinterpret_cast<const float4*>(&so[w][qh][d]);
+                const float4 v = *reinterpret_cast<const float4*>(so + (w * QT + qh) * (D + 4) + d);
                 ll += sl[w][qh] * f;
                 acc.x += v.x * f;
                 acc.y += v.y * f;
@@ -597,12 +767,13 @@ __global__ void __launch_bounds__(kAttnThreads, MINB) paged_attention_kernel(Att
             if (whole) {
                 const float r = ll == 0.0f ? 0.0f : 1.0f / ll;
                 *reinterpret_cast<uint2*>(a.y + ((int64_t)b * a.Hq + q0 + qh) * D + d) =
-                    make_uint2(pack_bf16x2(acc.x * r, acc.y * r), pack_bf16x2(acc.z * r, acc.w * r));
+                    make_uint2(cvt_bf16x2(acc.x * r, acc.y * r), cvt_bf16x2(acc.z * r, acc.w * r));
             } else {
                 *reinterpret_cast<float4*>(a.part_o + (pbase + qh) * D + d) = acc;
                 if (d == 0) a.part_ml[pbase + qh] = make_float2(mm, ll);
             }
         }
+        __syncthreads();   // before the next segment's copies and query
         u += seg;
     }
     if (bad) record_error(W8A8_ERR_INVALID_ARG, (kKernelIdAttn << 16) | 1);
@@ -643,14 +814,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a) {
     total = (red[1][0] + red[1][1] + red[1][2] + red[1][3]) * heads;
     const int64_t nb = (attn_len(a, b) + CH - 1) / CH;
     const int64_t us = before * heads + hq * nb, ue = us + nb;   // this unit's chunks
-    // CTA whose share [total i / grid, total (i + 1) / grid) holds chunk x
-    auto owner = [&](int64_t x) -> int {
-        int i = (int)(x * a.grid / total);
-        while (i > 0 && total * i / a.grid > x) --i;
-        while (i + 1 < a.grid && total * (i + 1) / a.grid <= x) ++i;
-        return i;
-    };
-    const int i0 = nb ? owner(us) : 0, i1 = nb ? owner(ue - 1) : 0;
+    const int64_t per = (total + a.grid - 1) / a.grid;
+    const int i0 = nb ? (int)(us / per) : 0, i1 = nb ? (int)((ue - 1) / per) : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (nb && i0 == i1) return;   // written by its CTA
     for (int i = threadIdx.x; i < nq * (D / 4); i += 128) {
@@ -658,13 +823,10 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a) {
         float mm = -INFINITY, ll = 0.0f;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (nb) {
-            // a share of no chunks (fewer chunks than CTAs) leaves no part
             for (int k = i0; k <= i1; ++k)
-                if (total * k / a.grid < total * (k + 1) / a.grid)
-                    mm = fmaxf(mm, __ldcg(&a.part_ml[((int64_t)k * 2 + (k == i0 ? 1 : 0)) * QT + qh]).x);
+                mm = fmaxf(mm, __ldcg(&a.part_ml[((int64_t)k * 2 + (k == i0 ? 1 : 0)) * QT + qh]).x);
             const float mu = mm == -INFINITY ? 0.0f : mm;
             for (int k = i0; k <= i1; ++k) {
-                if (total * k / a.grid == total * (k + 1) / a.grid) continue;
                 const int64_t p = ((int64_t)k * 2 + (k == i0 ? 1 : 0)) * QT + qh;
                 const float2 ml = __ldcg(&a.part_ml[p]);
                 const float f = attn_ex2(ml.x - mu);
@@ -678,7 +840,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a) {
         }
         const float r = ll == 0.0f ? 0.0f : 1.0f / ll;
         *reinterpret_cast<uint2*>(a.y + ((int64_t)b * a.Hq + q0 + qh) * D + d) =
-            make_uint2(pack_bf16x2(acc.x * r, acc.y * r), pack_bf16x2(acc.z * r, acc.w * r));
+            make_uint2(cvt_bf16x2(acc.x * r, acc.y * r), cvt_bf16x2(acc.z * r, acc.w * r));
     }
 }
 

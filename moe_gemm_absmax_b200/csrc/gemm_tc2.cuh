@@ -43,7 +43,7 @@ constexpr int kKernelIdGemmTc2 = 4;
 // per-stage hand-off (MMA completion -> empty -> producer -> full -> MMA
 // thread): one k block for the 256 and 160 tiles (512 / 320 cycles of MMA),
 // two for the 144 tile (2 x 288).
-template <int BN>
+template <int BN, bool FUSED = false>
 struct Tc2Smem {
     // k blocks per stage: the 144 tile (a few hundred tokens, one tile per
     // cluster) takes two, halving the stage hand-offs per MMA
@@ -52,15 +52,17 @@ struct Tc2Smem {
     static constexpr int kB1 = (BN / 2) * kTcBK;             // one k block of B: 16 / 10 / 9 KB (multiples of 1 KB)
     static constexpr int kA = kKB * kA1;
     static constexpr int kB = kKB * kB1;
-    static constexpr int kStages = BN == 256 ? 6 : (BN == 144 ? 4 : 8);
+    static constexpr int kStages = BN == 256 ? 6 : (BN == 144 ? 4 : (FUSED ? 7 : 8));
     static constexpr int kTiles = kStages * (kA + kB);
     static constexpr int kBars = (2 * kStages + 2 + 2 + 1) * 8;
     // each epilogue warp's copy of the tile's column scales (fp32)
     static constexpr int kEpiOff = kTiles + (kBars + 16 + 15) / 16 * 16;
-    static constexpr int kEpiBytes = kTc2Epi * BN * 4;
+    // (FUSED: each warp's 32 rows x 32 columns of bf16 on their way in or out,
+    // and the chunk's 32 column scales and biases)
+    static constexpr int kEpiWarp = FUSED ? 32 * 64 + 2 * 32 * 4 : BN * 4;
+    static constexpr int kEpiBytes = kTc2Epi * kEpiWarp;
     static constexpr int kBytes = 1024 + kEpiOff + kEpiBytes;
-    static constexpr int kBytesFused = kBytes + kEpiBytes;   // kEpiFused: the same again for the biases
-    static_assert(kBytesFused <= 227 * 1024, "shared memory per CTA");
+    static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -88,13 +90,6 @@ __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorM
         "%4}], [%2];" ::"r"(smem_u32(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(x), "r"(y)
         : "memory");
-}
-
-// Two fp32 values to bf16 (round to nearest even each) packed lo | hi << 16, one instruction.
-__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
 }
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t mbar) {
@@ -134,7 +129,7 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
     static_assert(EPI == kEpiBf16 || EPI == kEpiS32 || EPI == kEpiMoeGated || EPI == kEpiFused, "dense epilogues");
     static_assert(BN % 16 == 0 && (BN / 2) % 8 == 0 && BN <= 256, "pair tile width");
     constexpr int kCols = 2 * BN <= 256 ? 256 : 512;   // two accumulators of BN columns (a power of two)
-    using SM = Tc2Smem<BN>;
+    using SM = Tc2Smem<BN, EPI == kEpiFused>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
@@ -275,8 +270,7 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
         const int quarter = warp & 3;              // TMEM lanes [32 q, 32 q + 32)
         const int chalf = (warp - 2) >> 2;         // chunks c = 32 chalf + 64 i
         const uint32_t tempty_leader0 = mapa_shared(smem_u32(&tempty[0]), 0);
-        float* sw_s = epi_scratch + (warp - 2) * BN;   // this warp's copy of the tile's column scales
-        float* bias_s = sw_s + SM::kEpiBytes / 4;      // kEpiFused: and of its biases
+        float* sw_s = epi_scratch + (warp - 2) * (SM::kEpiWarp / 4);   // this warp's copy of the tile's column scales
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int tile = cluster_id; tile < num_tiles; tile += nclusters) {
@@ -285,7 +279,7 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
             const bool row_ok = row < p.M;
             float sxr = 0.0f;
             if ((EPI == kEpiBf16 || EPI == kEpiMoeGated || EPI == kEpiFused) && row_ok) sxr = __ldg(p.sx + row);
-            if (EPI == kEpiBf16 || EPI == kEpiMoeGated || EPI == kEpiFused) {
+            if (EPI == kEpiBf16 || EPI == kEpiMoeGated) {
                 // the tile's BN column scales (N % 8 == 0: a 4-column vector is all in or all out)
                 __syncwarp();   // the previous tile's reads are done
                 for (int v = lane; v < BN / 4; v += 32) {
@@ -293,44 +287,46 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
                     float4 sv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     if (n < p.N) sv = __ldg(reinterpret_cast<const float4*>(p.sw + n));
                     *reinterpret_cast<float4*>(sw_s + 4 * v) = sv;
-                    if (EPI == kEpiFused) {
-                        float4 bv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (p.f.bias && n < p.N) bv = __ldg(reinterpret_cast<const float4*>(p.f.bias + n));
-                        *reinterpret_cast<float4*>(bias_s + 4 * v) = bv;
-                    }
                 }
                 __syncwarp();
             }
-            // residual of one 32-column chunk, in flight with the chunk's TMEM load
-            auto load_res = [&](uint4 (&q)[4], int c) {
-                if (EPI != kEpiFused) return;
+            // kEpiFused: global memory is read and written 64 bytes a row, eight rows
+            // an instruction (lane = 4 row + 16-byte unit); the warp's 32 x 32 chunk
+            // changes hands with the accumulator's layout (lane = row) through 2 KB
+            // of shared memory whose units are XORed with the row pair, so that
+            // neither side has bank conflicts.  The tile's residual is all in
+            // flight before the accumulator is waited for.
+            constexpr int kChunks = (BN + 63) / 64;
+            const int frow = mt * kTc2BM + (int)rank * 128 + quarter * 32 + (lane >> 2);   // + 8 v
+            const int fcol = nt * BN + 32 * chalf + 8 * (lane & 3);                        // + 64 i
+            uint4 res[EPI == kEpiFused ? kChunks : 1][4];
+            float swc[EPI == kEpiFused ? kChunks : 1], bic[EPI == kEpiFused ? kChunks : 1];
+            if constexpr (EPI == kEpiFused) {
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    q[v] = make_uint4(0, 0, 0, 0);
-                    if (p.f.res && row_ok && c + v * 8 < BN && nt * BN + c + v * 8 < p.N)
-                        q[v] = ld_residual16(p.f.res + (int64_t)row * p.f.ldr + nt * BN + c + v * 8);
+                for (int i = 0; i < kChunks; ++i) {
+                    const bool col_ok = 32 * chalf + 64 * i + 8 * (lane & 3) < BN && fcol + 64 * i < p.N;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        res[i][v] = make_uint4(0, 0, 0, 0);
+                        if (p.f.res && col_ok && frow + 8 * v < p.M)
+                            res[i][v] = ld_residual16(p.f.res + (int64_t)(frow + 8 * v) * p.f.ldr + fcol + 64 * i);
+                    }
+                    const int n = nt * BN + 32 * chalf + 64 * i + lane;
+                    swc[i] = n < p.N ? __ldg(p.sw + n) : 0.0f;
+                    bic[i] = p.f.bias && n < p.N ? __ldg(p.f.bias + n) : 0.0f;
                 }
-            };
-            uint4 qa[4], qb[4];
-            load_res(qa, 32 * chalf);
+            }
             if (!mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, (kKernelIdGemmTc2 << 16) | 6)) break;
             tc_fence_after();
             const uint32_t tq = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN);
             // one 32-column chunk: convert and store (the next chunk's TMEM load is in flight)
-            auto chunk = [&](const uint32_t (&r)[32], const uint4 (&q)[4], int c) {
+            auto chunk = [&](const uint32_t (&r)[32], int c) {
                 const int n0 = nt * BN + c;
                 if (!row_ok || n0 >= p.N) return;
                 // the tile's columns in this chunk (BN % 32 == 16: the last chunk holds
                 // 16; its TMEM load reads 16 columns past the tile, which are ignored)
                 const int ncol = BN - c < 32 ? BN - c : 32;
-                if (EPI == kEpiFused) {
-                    uint16_t* yrow = reinterpret_cast<uint16_t*>(p.out) + (int64_t)row * p.f.ldy;
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        if (v * 8 < ncol && n0 + v * 8 < p.N)
-                            *reinterpret_cast<uint4*>(yrow + n0 + v * 8) =
-                                epi_fused8(r + v * 8, sxr, sw_s + c + v * 8, bias_s + c + v * 8, q[v], p.f.act);
-                } else if (EPI == kEpiBf16) {
+                if (EPI == kEpiBf16) {
                     uint16_t* yrow = reinterpret_cast<uint16_t*>(p.out) + (int64_t)row * p.N;
                     const uint64_t sx2 = f2_pack(sxr, sxr);
 #pragma unroll
@@ -378,24 +374,52 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
                 }
             };
             uint32_t ra[32], rb[32];
-            int c = 32 * chalf;
-            if (c < BN) tmem_ld_32x32b_x32(tq + (uint32_t)c, ra);
-            while (c < BN) {
-                tc_wait_ld();
-                if (c + 64 < BN) {
-                    tmem_ld_32x32b_x32(tq + (uint32_t)(c + 64), rb);
-                    load_res(qb, c + 64);
+            if constexpr (EPI == kEpiFused) {
+                uint4* ex = reinterpret_cast<uint4*>(sw_s);          // [32 rows][4 units]
+                float* sb = sw_s + 32 * 64 / 4;                      // 32 scales, 32 biases
+                const int mine = lane * 4, mx = (lane >> 1) & 3;     // row `lane`
+                const int gx = lane ^ ((lane >> 3) & 3);             // row lane / 4 + 8 v, unit lane % 4: 32 v + gx
+                tmem_ld_32x32b_x32(tq + (uint32_t)(32 * chalf), ra);
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+                    const int c = 32 * chalf + 64 * i;
+                    if (c >= BN) break;
+                    __syncwarp();   // the previous chunk has left
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) ex[32 * v + gx] = res[i][v];
+                    sb[lane] = swc[i];
+                    sb[32 + lane] = bic[i];
+                    __syncwarp();
+                    tc_wait_ld();
+                    if (c + 64 < BN) tmem_ld_32x32b_x32(tq + (uint32_t)(c + 64), (i & 1) ? ra : rb);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        ex[mine + (v ^ mx)] = epi_fused8(((i & 1) ? rb : ra) + 8 * v, sxr, sb + 8 * v, sb + 32 + 8 * v,
+                                                         ex[mine + (v ^ mx)], p.f.act);
+                    __syncwarp();
+                    if (c + 8 * (lane & 3) < BN && fcol + 64 * i < p.N) {
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            if (frow + 8 * v < p.M)
+                                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) +
+                                                          (int64_t)(frow + 8 * v) * p.f.ldy + fcol + 64 * i) =
+                                    ex[32 * v + gx];
+                    }
                 }
-                chunk(ra, qa, c);
-                c += 64;
-                if (c >= BN) break;
-                tc_wait_ld();
-                if (c + 64 < BN) {
-                    tmem_ld_32x32b_x32(tq + (uint32_t)(c + 64), ra);
-                    load_res(qa, c + 64);
+            } else {
+                int c = 32 * chalf;
+                if (c < BN) tmem_ld_32x32b_x32(tq + (uint32_t)c, ra);
+                while (c < BN) {
+                    tc_wait_ld();
+                    if (c + 64 < BN) tmem_ld_32x32b_x32(tq + (uint32_t)(c + 64), rb);
+                    chunk(ra, c);
+                    c += 64;
+                    if (c >= BN) break;
+                    tc_wait_ld();
+                    if (c + 64 < BN) tmem_ld_32x32b_x32(tq + (uint32_t)(c + 64), ra);
+                    chunk(rb, c);
+                    c += 64;
                 }
-                chunk(rb, qb, c);
-                c += 64;
             }
             tc_fence_before();
             __syncwarp();

@@ -117,16 +117,15 @@ int launch_tc(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st) {
 // Pair-tile GEMM (cta_group::2, 256 x BN tiles over two SMs).
 template <int EPI, int BN>
 int launch_tc2_bn(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st) {
-    using SM = Tc2Smem<BN>;
+    using SM = Tc2Smem<BN, EPI == kEpiFused>;
     auto kern = gemm_i8_tc2_kernel<EPI, BN>;
-    constexpr int kBytes = EPI == kEpiFused ? SM::kBytesFused : SM::kBytes;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return W8A8_ERR_CUDA;
     if (dev < 0 || dev >= kMaxDevices) return W8A8_ERR_UNSUPPORTED;
     static int max_clusters[kMaxDevices] = {0};
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kTc2Threads, 1, 1);
-    cfg.dynamicSmemBytes = kBytes;
+    cfg.dynamicSmemBytes = SM::kBytes;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -136,7 +135,7 @@ int launch_tc2_bn(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st)
     cfg.attrs = at;
     cfg.numAttrs = 1;
     if (max_clusters[dev] == 0) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes) != cudaSuccess)
             return W8A8_ERR_CUDA;
         cfg.gridDim = dim3((unsigned)(2 * (device_sms(dev) / 2)), 1, 1);
         int n = 0;
@@ -1550,26 +1549,31 @@ bool cache_shape_ok(int Hkv, int D, int64_t num_pages, int page_size) {
            Hkv <= 1024 && num_pages < (int64_t)1 << 31;
 }
 
-// Query tiles a pass and CTAs per SM by the registers a thread needs: output
-// sums NQ * D / 4, a tile's keys and values, the query.
-constexpr int attn_minb(int D, bool int8, int nq) {
-    return D == 256 ? 2 : (nq == 2 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 3));
-}
-// 16 query heads a pass where more than 8 share a key-value head, except at
-// D = 256, whose output sums would not fit the register file.
-int attn_nq(int G, int D) { return G > 8 && D < 256 ? 2 : 1; }
+// Up to 16 query heads share a pass over the cache.
+int attn_nq(int G) { return G > 8 ? 2 : 1; }
 constexpr int kAttnSms = 148;   // the work split's grid is fixed, so that workspace sizes are
+constexpr int kAttnMaxMinB = 3;
 
-size_t attn_part_rows(int D, int nq) { return (size_t)kAttnSms * attn_minb(D, true, nq) * 2 * 8 * nq; }
+size_t attn_part_rows(int nq) { return (size_t)kAttnSms * kAttnMaxMinB * 2 * 8 * nq; }
 
 template <int D, bool INT8, int NQ>
 int launch_attn(AttnArgs a, cudaStream_t st) {
-    constexpr int kMinB = attn_minb(D, INT8, NQ);
-    constexpr int CH = kAttnWarps * attn_tt<D, INT8>();
+    using Cfg = AttnCfg<D, INT8, NQ>;
+    static_assert(Cfg::kMinB <= kAttnMaxMinB, "workspace");
+    auto kern = paged_attention_kernel<D, INT8, NQ>;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return W8A8_ERR_CUDA;
+    if (dev < 0 || dev >= kMaxDevices) return W8A8_ERR_UNSUPPORTED;
+    static bool attr_done[kMaxDevices] = {false};
+    if (!attr_done[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kBytes) != cudaSuccess)
+            return W8A8_ERR_CUDA;
+        attr_done[dev] = true;
+    }
     const int64_t heads = (int64_t)a.Hkv * a.qtiles;
-    const int64_t most = (int64_t)a.B * heads * ((a.cap + CH - 1) / CH);   // chunks, if every sequence were full
-    a.grid = (int)(most < kAttnSms * kMinB ? (most > 0 ? most : 1) : kAttnSms * kMinB);
-    paged_attention_kernel<D, INT8, NQ, kMinB><<<(unsigned)a.grid, kAttnThreads, 0, st>>>(a);
+    const int64_t most = (int64_t)a.B * heads * ((a.cap + Cfg::CH - 1) / Cfg::CH);   // chunks, if every sequence were full
+    a.grid = (int)(most < kAttnSms * Cfg::kMinB ? most : kAttnSms * Cfg::kMinB);
+    kern<<<(unsigned)a.grid, kAttnThreads, Cfg::kBytes, st>>>(a);
     int rc = last_launch_status();
     if (rc != W8A8_OK) return rc;
     cudaLaunchConfig_t cfg = {};
@@ -1578,15 +1582,12 @@ int launch_attn(AttnArgs a, cudaStream_t st) {
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     pdl_config(cfg, at, true);
-    return cuda_status(cudaLaunchKernelEx(&cfg, attn_join_kernel<D, CH, NQ>, a));
+    return cuda_status(cudaLaunchKernelEx(&cfg, attn_join_kernel<D, Cfg::CH, NQ>, a));
 }
 
 template <int D, bool INT8>
 int launch_attn_nq(const AttnArgs& a, cudaStream_t st) {
-    if constexpr (D < 256) {
-        if (attn_nq(a.G, D) == 2) return launch_attn<D, INT8, 2>(a, st);
-    }
-    return launch_attn<D, INT8, 1>(a, st);
+    return attn_nq(a.G) == 2 ? launch_attn<D, INT8, 2>(a, st) : launch_attn<D, INT8, 1>(a, st);
 }
 
 template <int D, bool INT8>
@@ -1607,8 +1608,8 @@ int w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ld
     if ((k_scale == nullptr) != (v_scale == nullptr)) return W8A8_ERR_INVALID_ARG;
     if (!cache_shape_ok(Hkv, D, num_pages, page_size) || T > (int64_t)1 << 30) return W8A8_ERR_UNSUPPORTED;
     if (ldk < (int64_t)Hkv * D || ldv < (int64_t)Hkv * D || ldk % 8 != 0 || ldv % 8 != 0) return W8A8_ERR_INVALID_ARG;
-    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 8) ||
-        !aligned(v_scale, 8) || !aligned(slots, 8))
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 16) ||
+        !aligned(v_scale, 16) || !aligned(slots, 8))
         return W8A8_ERR_INVALID_ARG;
     if (T * Hkv * (D / 8) / 256 >= 0x7fffffffLL) return W8A8_ERR_UNSUPPORTED;
     KvAppendArgs a;
@@ -1629,7 +1630,7 @@ int w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ld
 
 size_t w8a8_paged_attention_workspace_size(int64_t B, int Hq, int Hkv, int D) {
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128 && D != 256)) return 0;
-    const size_t rows = attn_part_rows(D, attn_nq(Hq / Hkv, D));
+    const size_t rows = attn_part_rows(attn_nq(Hq / Hkv));
     return align_up(rows * D * 4, 256) + align_up(rows * 8, 256);
 }
 
@@ -1645,8 +1646,8 @@ int w8a8_paged_attention(const uint16_t* q, int64_t ldq, const void* k_cache, co
         Hq > (1 << 16))
         return W8A8_ERR_UNSUPPORTED;
     if (ldq < (int64_t)Hq * D || ldq % 8 != 0) return W8A8_ERR_INVALID_ARG;
-    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 8) ||
-        !aligned(v_scale, 8) || !aligned(block_table, 4) || !aligned(lengths, 4) || !aligned(y, 16) || !aligned(ws, 256))
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 16) ||
+        !aligned(v_scale, 16) || !aligned(block_table, 4) || !aligned(lengths, 4) || !aligned(y, 16) || !aligned(ws, 256))
         return W8A8_ERR_INVALID_ARG;
     if (ws_bytes < w8a8_paged_attention_workspace_size(B, Hq, Hkv, D)) return W8A8_ERR_WORKSPACE;
     AttnArgs a;
@@ -1664,13 +1665,13 @@ int w8a8_paged_attention(const uint16_t* q, int64_t ldq, const void* k_cache, co
     a.Hq = Hq;
     a.Hkv = Hkv;
     a.G = Hq / Hkv;
-    const int nq = attn_nq(a.G, D);
+    const int nq = attn_nq(a.G);
     a.qtiles = (a.G + 8 * nq - 1) / (8 * nq);
     a.num_pages = num_pages;
     a.page_shift = log2_exact(page_size);
     a.cap = max_pages << a.page_shift;
     a.scale_log2 = scale * kLog2e;
-    const size_t rows = attn_part_rows(D, nq);
+    const size_t rows = attn_part_rows(nq);
     a.part_o = reinterpret_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(ws) + align_up(rows * D * 4, 256));
     a.grid = 0;
