@@ -782,12 +782,18 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
             if (__ldg(a.lengths + i) > a.cap) record_error(W8A8_ERR_INVALID_ARG, (kKernelIdAttn << 16) | 2);
 }
 
-// Joins the parts of the (sequence, head) units that several CTAs shared, in
-// CTA order, and writes the zeros of empty sequences.  One CTA per unit.
+// Joins the parts of the (sequence, head) units that several CTAs shared, and
+// writes the zeros of empty sequences.  Blocks (x, y): unit x, slice y of its
+// outputs, four d's a thread; threads beyond the slice's take every NG-th part
+// and meet in shared memory in a fixed order.  Latency is all that this kernel
+// costs, so the loads of four parts are in flight at a time.
+constexpr int kAttnJoinThreads = 256;
 template <int D, int CH, int NQ>
-__global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a) {
-    constexpr int QT = 8 * NQ;
-    __shared__ int64_t red[2][4];
+__global__ void __launch_bounds__(kAttnJoinThreads) attn_join_kernel(AttnArgs a, int per_cta) {
+    constexpr int QT = 8 * NQ, NT = kAttnJoinThreads;
+    __shared__ int64_t red[2][NT / 32];
+    __shared__ float4 racc[NT];
+    __shared__ float2 rml[NT];
     const int64_t heads = (int64_t)a.Hkv * a.qtiles;
     const int b = (int)(blockIdx.x / heads), hq = (int)(blockIdx.x - b * heads);
     const int h = hq / a.qtiles, qt = hq - h * a.qtiles;
@@ -795,7 +801,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a) {
     const int q0 = h * a.G + qt * QT;
     // chunks before this sequence, and in all
     int64_t before = 0, total = 0;
-    for (int i = threadIdx.x; i < a.B; i += 128) {
+    for (int i = threadIdx.x; i < a.B; i += NT) {
         const int64_t n = (attn_len(a, i) + CH - 1) / CH;
         total += n;
         if (i < b) before += n;
@@ -810,38 +816,65 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a) {
         red[1][threadIdx.x >> 5] = total;
     }
     __syncthreads();
-    before = red[0][0] + red[0][1] + red[0][2] + red[0][3];
-    total = (red[1][0] + red[1][1] + red[1][2] + red[1][3]) * heads;
+    before = total = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) {
+        before += red[0][i];
+        total += red[1][i];
+    }
+    total *= heads;
     const int64_t nb = (attn_len(a, b) + CH - 1) / CH;
     const int64_t us = before * heads + hq * nb, ue = us + nb;   // this unit's chunks
     const int64_t per = (total + a.grid - 1) / a.grid;
-    const int i0 = nb ? (int)(us / per) : 0, i1 = nb ? (int)((ue - 1) / per) : 0;
+    const int i0 = nb ? (int)(us / per) : 0, i1 = nb ? (int)((ue - 1) / per) : -1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (nb && i0 == i1) return;   // written by its CTA
-    for (int i = threadIdx.x; i < nq * (D / 4); i += 128) {
-        const int qh = i / (D / 4), d = 4 * (i - qh * (D / 4));
-        float mm = -INFINITY, ll = 0.0f;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (nb) {
-            for (int k = i0; k <= i1; ++k)
-                mm = fmaxf(mm, __ldcg(&a.part_ml[((int64_t)k * 2 + (k == i0 ? 1 : 0)) * QT + qh]).x);
-            const float mu = mm == -INFINITY ? 0.0f : mm;
-            for (int k = i0; k <= i1; ++k) {
-                const int64_t p = ((int64_t)k * 2 + (k == i0 ? 1 : 0)) * QT + qh;
-                const float2 ml = __ldcg(&a.part_ml[p]);
-                const float f = attn_ex2(ml.x - mu);
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + p * D + d));
-                ll += ml.y * f;
-                acc.x += v.x * f;
-                acc.y += v.y * f;
-                acc.z += v.z * f;
-                acc.w += v.w * f;
+    const int item = threadIdx.x % per_cta, grp = threadIdx.x / per_cta, ng = NT / per_cta;
+    const int i = blockIdx.y * per_cta + item;
+    const int qh = i / (D / 4), d = 4 * (i - qh * (D / 4));
+    float mm = -INFINITY, ll = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](const float2& ml, const float4& v) {
+        const float mn = fmaxf(mm, ml.x);
+        const float mu = mn == -INFINITY ? 0.0f : mn;
+        const float f0 = attn_ex2(mm - mu), f = attn_ex2(ml.x - mu);
+        mm = mn;
+        ll = ll * f0 + ml.y * f;
+        acc.x = acc.x * f0 + v.x * f;
+        acc.y = acc.y * f0 + v.y * f;
+        acc.z = acc.z * f0 + v.z * f;
+        acc.w = acc.w * f0 + v.w * f;
+    };
+    if (qh < nq) {
+        for (int k = i0 + grp; k <= i1; k += 4 * ng) {
+            float2 ml[4];
+            float4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int kk = k + j * ng;
+                const int64_t p = ((int64_t)kk * 2 + (kk == i0 ? 1 : 0)) * QT + qh;
+                ml[j] = make_float2(-INFINITY, 0.0f);
+                v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (kk <= i1) {
+                    ml[j] = __ldcg(&a.part_ml[p]);
+                    v[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + p * D + d));
+                }
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) add(ml[j], v[j]);
         }
-        const float r = ll == 0.0f ? 0.0f : 1.0f / ll;
-        *reinterpret_cast<uint2*>(a.y + ((int64_t)b * a.Hq + q0 + qh) * D + d) =
-            make_uint2(cvt_bf16x2(acc.x * r, acc.y * r), cvt_bf16x2(acc.z * r, acc.w * r));
     }
+    if (ng > 1) {
+        racc[threadIdx.x] = acc;
+        rml[threadIdx.x] = make_float2(mm, ll);
+        __syncthreads();
+        if (grp != 0) return;
+        for (int j = 1; j < ng; ++j) add(rml[j * per_cta + item], racc[j * per_cta + item]);
+    }
+    if (qh >= nq) return;
+    const float r = ll == 0.0f ? 0.0f : 1.0f / ll;
+    *reinterpret_cast<uint2*>(a.y + ((int64_t)b * a.Hq + q0 + qh) * D + d) =
+        make_uint2(cvt_bf16x2(acc.x * r, acc.y * r), cvt_bf16x2(acc.z * r, acc.w * r));
 }
 
 }  // namespace w8a8

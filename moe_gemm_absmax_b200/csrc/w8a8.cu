@@ -1576,13 +1576,18 @@ int launch_attn(AttnArgs a, cudaStream_t st) {
     kern<<<(unsigned)a.grid, kAttnThreads, Cfg::kBytes, st>>>(a);
     int rc = last_launch_status();
     if (rc != W8A8_OK) return rc;
+    // few units have many parts each: more slices of their outputs, so that
+    // more threads share the parts (down to a warp's worth of outputs a CTA)
+    constexpr int kItems = 8 * NQ * D / 4;
+    int per_cta = kItems < kAttnJoinThreads ? kItems : kAttnJoinThreads;
+    while (per_cta > 32 && a.B * heads * (kItems / per_cta) < 4 * kAttnSms) per_cta /= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.B * heads), 1, 1);
-    cfg.blockDim = dim3(128, 1, 1);
+    cfg.gridDim = dim3((unsigned)(a.B * heads), (unsigned)(kItems / per_cta), 1);
+    cfg.blockDim = dim3(kAttnJoinThreads, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     pdl_config(cfg, at, true);
-    return cuda_status(cudaLaunchKernelEx(&cfg, attn_join_kernel<D, Cfg::CH, NQ>, a));
+    return cuda_status(cudaLaunchKernelEx(&cfg, attn_join_kernel<D, Cfg::CH, NQ>, a, per_cta));
 }
 
 template <int D, bool INT8>
@@ -1708,7 +1713,7 @@ int w8a8_token_logprobs(const void* logits, int logits_f32, int64_t ld, const in
     a.topk = topk;
     const int64_t windows = (V * (logits_f32 ? 4 : 2) + 15) / 16;
     int C = 8;
-    while (C > 1 && (M * C > 2 * current_sms() || windows < (int64_t)C * kLpThreads)) C /= 2;
+    while (C > 1 && (M * C > 4 * current_sms() || windows < (int64_t)C * kLpThreads)) C /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(M * C), 1, 1);
     cfg.blockDim = dim3(kLpThreads, 1, 1);
