@@ -20,82 +20,145 @@ struct EpiFused {
     int act;               // W8A8_ACT_*
 };
 
-// 1 / (1 + e^-t): ex2.approx and a division good to 2 ulp, which leaves the
-// result within 2^-21 of its value, 1/4096 of a bf16 rounding step.  Far left
-// e^-t overflows to infinity and the quotient is 0, the limit.
-__device__ __forceinline__ float fast_sigmoid(float t) { return __fdividef(1.0f, 1.0f + __expf(-t)); }
+// Activations on two values at a time (sm_100 adds and multiplies pairs of
+// fp32 in one instruction).  1 / (1 + e^-t) from ex2.approx and rcp.approx,
+// good to 2 ulp each, which leaves it within 2^-20 of its value, 1/4096 of a
+// bf16 rounding step.  Far left e^-t overflows to infinity and the quotient is
+// 0, the limit.
+__device__ __forceinline__ float epi_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float epi_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t f2_const(float c) { return f2_pack(c, c); }
+__device__ __forceinline__ uint64_t f2_ex2(uint64_t x) {
+    float a, b;
+    f2_unpack(x, a, b);
+    return f2_pack(epi_ex2(a), epi_ex2(b));
+}
+__device__ __forceinline__ uint64_t f2_rcp(uint64_t x) {
+    float a, b;
+    f2_unpack(x, a, b);
+    return f2_pack(epi_rcp(a), epi_rcp(b));
+}
+// sigmoid(t) with t given times -log2 e
+__device__ __forceinline__ uint64_t f2_sigmoid(uint64_t mt) { return f2_rcp(f2_add(f2_ex2(mt), f2_const(1.0f))); }
 
+__device__ __forceinline__ uint64_t act_relu(uint64_t v) {
+    float a, b;
+    f2_unpack(v, a, b);
+    return f2_pack(fmaxf(a, 0.0f), fmaxf(b, 0.0f));
+}
+__device__ __forceinline__ uint64_t act_silu(uint64_t v) {
+    return f2_mul(v, f2_sigmoid(f2_mul(v, f2_const(-1.4426950408889634f))));
+}
+// (1 + tanh u) / 2 = sigmoid(2u), u = sqrt(2/pi) (v + 0.044715 v^3)
+__device__ __forceinline__ uint64_t act_gelu_tanh(uint64_t v) {
+    const uint64_t w = f2_fma(f2_mul(f2_mul(v, v), f2_const(0.044715f)), v, v);
+    return f2_mul(v, f2_sigmoid(f2_mul(w, f2_const(-2.302208198f))));   // -2 sqrt(2/pi) log2 e
+}
 // v * Phi(v).  With a = |v|, Phi(-a) = e^(-a^2 / 2) erfcx(a / sqrt 2) / 2, the
 // scaled complementary error function as t times a polynomial of degree 6 in
 // t = 1 / (1 + 0.375 a / sqrt 2), fitted to the least largest relative error
 // over a / sqrt 2 in [0, 10.5] (6.4e-7): the left tail keeps its digits, which
-// 1 + erf would lose to cancellation, at half the instructions of normcdff
-// and without its branches.
-__device__ __forceinline__ float gelu_erf(float v) {
-    const float a = fabsf(v);
-    const float t = __fdividef(1.0f, __fmaf_rn(a, 0.26516504294495535f, 1.0f));
-    float p = -1.350962669e-01f;
-    p = __fmaf_rn(p, t, 3.879391849e-01f);
-    p = __fmaf_rn(p, t, -1.295993030e-01f);
-    p = __fmaf_rn(p, t, 2.830630541e-01f);
-    p = __fmaf_rn(p, t, 1.666639745e-01f);
-    p = __fmaf_rn(p, t, 2.156893015e-01f);
-    p = __fmaf_rn(p, t, 2.113394439e-01f);
-    const float q = 0.5f * p * t * __expf(-0.5f * a * a);   // Phi(-a)
-    return v * (v < 0.0f ? q : 1.0f - q);
+// 1 + erf would lose to cancellation, without normcdff's branches (M = 4096,
+// K = 5120, N = 17408: 360 us with normcdff).
+__device__ __forceinline__ uint64_t act_gelu(uint64_t v) {
+    float v0, v1;
+    f2_unpack(v, v0, v1);
+    const uint64_t a = f2_pack(fabsf(v0), fabsf(v1));
+    const uint64_t t = f2_rcp(f2_fma(a, f2_const(0.26516504294495535f), f2_const(1.0f)));
+    uint64_t p = f2_fma(f2_const(-0.135096266866f), t, f2_const(0.387939184904f));
+    p = f2_fma(p, t, f2_const(-0.129599303007f));
+    p = f2_fma(p, t, f2_const(0.283063054085f));
+    p = f2_fma(p, t, f2_const(0.166663974524f));
+    p = f2_fma(p, t, f2_const(0.215689301491f));
+    p = f2_fma(p, t, f2_const(0.211339443922f));
+    const uint64_t e = f2_ex2(f2_mul(f2_mul(a, a), f2_const(-0.7213475204444817f)));
+    float q0, q1;
+    f2_unpack(f2_mul(f2_mul(p, f2_mul(t, f2_const(0.5f))), e), q0, q1);   // Phi(-a)
+    return f2_mul(v, f2_pack(v0 < 0.0f ? q0 : 1.0f - q0, v1 < 0.0f ? q1 : 1.0f - q1));
 }
 
-__device__ __forceinline__ float act_apply(int act, float v) {
-    switch (act) {
-        case W8A8_ACT_RELU: return fmaxf(v, 0.0f);
-        case W8A8_ACT_SILU: return v * fast_sigmoid(v);
-        case W8A8_ACT_GELU: return gelu_erf(v);
-        // (1 + tanh u) / 2 = sigmoid(2u)
-        case W8A8_ACT_GELU_TANH:
-            return v * fast_sigmoid(1.5957691216057308f * __fmaf_rn(0.044715f * v * v, v, v));
-        default: return v;
+// One branch for all of them, uniform over the grid.
+template <int N>
+__device__ __forceinline__ void act_apply(int act, uint64_t (&v)[N]) {
+    if (act == W8A8_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = act_silu(v[j]);
+    } else if (act == W8A8_ACT_RELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = act_relu(v[j]);
+    } else if (act == W8A8_ACT_GELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = act_gelu(v[j]);
+    } else if (act == W8A8_ACT_GELU_TANH) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = act_gelu_tanh(v[j]);
     }
 }
 
-// Eight consecutive columns of one row: int32 accumulators, the columns'
-// scales and biases (shared memory), the residual's 16 bytes -> 16 bytes of bf16.
+// v + residual (two bf16), to two bf16.
+__device__ __forceinline__ uint32_t epi_out2(uint64_t v, uint32_t res) {
+    float a, b;
+    f2_unpack(v, a, b);
+    return cvt_bf16x2(__fadd_rn(a, __uint_as_float(res << 16)), __fadd_rn(b, __uint_as_float(res & 0xffff0000u)));
+}
+
+// Bias after the two products, each rounded by itself: one fp32 at a time, as
+// mul.f32x2 followed by add.f32x2 came out with the single rounding of an fma
+// on sm_100a.
+__device__ __forceinline__ uint64_t epi_bias2(uint64_t v, float b0, float b1) {
+    float x, y;
+    f2_unpack(v, x, y);
+    return f2_pack(__fadd_rn(x, b0), __fadd_rn(y, b1));
+}
+
+// Four consecutive columns of one row: int32 accumulators, the columns' scales
+// and biases, the residual's 8 bytes -> 8 bytes of bf16.
+__device__ __forceinline__ uint2 epi_fused4(const int4& acc, float sx, const float4& sw, const float4& bias,
+                                            const uint2& res, int act) {
+    const uint64_t sx2 = f2_pack(sx, sx);
+    uint64_t v[2] = {f2_pack(__int2float_rn(acc.x), __int2float_rn(acc.y)), f2_pack(__int2float_rn(acc.z), __int2float_rn(acc.w))};
+    v[0] = epi_bias2(f2_mul(f2_mul(v[0], sx2), f2_pack(sw.x, sw.y)), bias.x, bias.y);
+    v[1] = epi_bias2(f2_mul(f2_mul(v[1], sx2), f2_pack(sw.z, sw.w)), bias.z, bias.w);
+    act_apply<2>(act, v);
+    return make_uint2(epi_out2(v[0], res.x), epi_out2(v[1], res.y));
+}
+
+// Eight, with scales and biases in shared memory and 16 bytes of residual.
 __device__ __forceinline__ uint4 epi_fused8(const uint32_t* r, float sx, const float* sw8, const float* bias8,
                                             const uint4& res, int act) {
-    float v[8];
+    const uint64_t sx2 = f2_pack(sx, sx);
+    uint64_t v[4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const float4 s = *reinterpret_cast<const float4*>(sw8 + 4 * h);
         const float4 b = *reinterpret_cast<const float4*>(bias8 + 4 * h);
-        const float sv[4] = {s.x, s.y, s.z, s.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v[4 * h + j] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * h + j]), sx), sv[j]), bv[j]);
+        const uint64_t a0 = f2_pack(__int2float_rn((int)r[4 * h]), __int2float_rn((int)r[4 * h + 1]));
+        const uint64_t a1 = f2_pack(__int2float_rn((int)r[4 * h + 2]), __int2float_rn((int)r[4 * h + 3]));
+        v[2 * h] = epi_bias2(f2_mul(f2_mul(a0, sx2), f2_pack(s.x, s.y)), b.x, b.y);
+        v[2 * h + 1] = epi_bias2(f2_mul(f2_mul(a1, sx2), f2_pack(s.z, s.w)), b.z, b.w);
     }
-    // one branch a vector, uniform over the grid
-    auto each = [&](auto f) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = f(v[j]);
-    };
-    if (act == W8A8_ACT_SILU) each([](float t) { return act_apply(W8A8_ACT_SILU, t); });
-    else if (act == W8A8_ACT_RELU) each([](float t) { return act_apply(W8A8_ACT_RELU, t); });
-    else if (act == W8A8_ACT_GELU) each([](float t) { return act_apply(W8A8_ACT_GELU, t); });
-    else if (act == W8A8_ACT_GELU_TANH) each([](float t) { return act_apply(W8A8_ACT_GELU_TANH, t); });
-    const uint32_t rw[4] = {res.x, res.y, res.z, res.w};
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        o[j] = pack_bf16x2(__fadd_rn(v[2 * j], __uint_as_float(rw[j] << 16)),
-                           __fadd_rn(v[2 * j + 1], __uint_as_float(rw[j] & 0xffff0000u)));
-    return make_uint4(o[0], o[1], o[2], o[3]);
+    act_apply<4>(act, v);
+    return make_uint4(epi_out2(v[0], res.x), epi_out2(v[1], res.y), epi_out2(v[2], res.z), epi_out2(v[3], res.w));
 }
 
 // One output, for the kernels that hold single columns.
 __device__ __forceinline__ uint16_t epi_fused1(int acc, float sx, float sw, const EpiFused& f, int64_t m, int n) {
-    float v = __fmul_rn(__fmul_rn(__int2float_rn(acc), sx), sw);
-    if (f.bias) v = __fadd_rn(v, __ldg(f.bias + n));
-    v = act_apply(f.act, v);
-    if (f.res) v = __fadd_rn(v, bf16_bits_to_float(__ldcg(f.res + m * f.ldr + n)));
-    return float_to_bf16_bits(v);
+    float x = __fmul_rn(__fmul_rn(__int2float_rn(acc), sx), sw);
+    if (f.bias) x = __fadd_rn(x, __ldg(f.bias + n));
+    uint64_t v[1] = {f2_pack(x, x)};
+    act_apply<1>(f.act, v);
+    float a, b;
+    f2_unpack(v[0], a, b);
+    if (f.res) a = __fadd_rn(a, bf16_bits_to_float(__ldcg(f.res + m * f.ldr + n)));
+    return float_to_bf16_bits(a);
 }
 
 // 16 bytes of the residual: coherent (it may be the output), past L1 (read once).

@@ -43,7 +43,7 @@ enum TcEpilogue : int {
     kEpiMoeGated = 3,
     kEpiMoeCombine = 4,        // w * y2 stored at (token, slot)
     kEpiMoeCombineAtomic = 5,  // w * y2 added atomically into the token's row
-    kEpiFused = 6              // bias, activation and residual, strided bf16 rows (epilogue.cuh)
+    kEpiFused = 6              // pair tiles: bias, activation and residual, strided bf16 rows (epilogue.cuh)
 };
 
 struct TcParams {
@@ -120,9 +120,6 @@ struct TcSmem {
     static constexpr int kEpiOff = kTiles + (kBars + 16 + 15) / 16 * 16;
     static constexpr int kEpiBytes = 8 * (BN > 64 ? BN : 64) * 4;
     static constexpr int kBytes = 1024 /*alignment slack*/ + kEpiOff + kEpiBytes;
-    // kEpiFused: the same again for the biases
-    static constexpr int kBytesFused = kBytes + kEpiBytes;
-    static_assert(kBytesFused <= 227 * 1024, "shared memory per CTA");
 };
 
 // NEPI epilogue warps: 4 (one per TMEM lane quarter) or 8 (two per quarter,
@@ -413,9 +410,8 @@ __global__ void __launch_bounds__(tc_threads<NEPI>(), 1)
                 // warp's shared scratch, before the wait: N % 8 == 0, so a 4-column
                 // vector is all in or all out
                 constexpr bool kSw = EPI == kEpiBf16 || EPI == kEpiMoeGated || EPI == kEpiMoeCombine ||
-                                     EPI == kEpiMoeCombineAtomic || EPI == kEpiFused;
+                                     EPI == kEpiMoeCombineAtomic;
                 float* sw_s = epi_scratch + (warp - 2) * BN;
-                float* bias_s = sw_s + SM::kEpiBytes / 4;   // kEpiFused
                 if (kSw) {
                     __syncwarp();   // the previous tile's reads are done
                     const float* swt = p.sw + (int64_t)ti.e * p.N;
@@ -424,30 +420,13 @@ __global__ void __launch_bounds__(tc_threads<NEPI>(), 1)
                         float4 sv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         if (n < p.N) sv = __ldg(reinterpret_cast<const float4*>(swt + n));
                         *reinterpret_cast<float4*>(sw_s + 4 * v) = sv;
-                        if (EPI == kEpiFused) {
-                            float4 bv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            if (p.f.bias && n < p.N) bv = __ldg(reinterpret_cast<const float4*>(p.f.bias + n));
-                            *reinterpret_cast<float4*>(bias_s + 4 * v) = bv;
-                        }
                     }
                     __syncwarp();
                 }
-                // residual of one 32-column chunk, in flight with the chunk's TMEM load
-                auto load_res = [&](uint4 (&q)[4], int c) {
-                    if (EPI != kEpiFused) return;
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        q[v] = make_uint4(0, 0, 0, 0);
-                        if (p.f.res && row_ok && nt * BN + c + v * 8 < p.N)
-                            q[v] = ld_residual16(p.f.res + (int64_t)row * p.f.ldr + nt * BN + c + v * 8);
-                    }
-                };
-                uint4 qa[4], qb[4];
-                load_res(qa, NEPI == 8 ? 32 * chalf : 0);
                 if (!mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, (kKernelIdGemmTc << 16) | 6)) break;
                 tc_fence_after();
                 float sxr = 0.0f;
-                if ((EPI == kEpiBf16 || EPI == kEpiFused || EPI == kEpiMoeGated || EPI == kEpiMoeCombine || EPI == kEpiMoeCombineAtomic) &&
+                if ((EPI == kEpiBf16 || EPI == kEpiMoeGated || EPI == kEpiMoeCombine || EPI == kEpiMoeCombineAtomic) &&
                     row_ok)
                     sxr = __ldg(p.sx + row);
                 int64_t orow_i = 0;
@@ -458,17 +437,10 @@ __global__ void __launch_bounds__(tc_threads<NEPI>(), 1)
                     wr = __ldg(p.row_w + row);
                 }
                 // one 32-column chunk (the next one's TMEM load is in flight)
-                auto chunk = [&](const uint32_t (&r)[32], const uint4 (&q)[4], int c) {
+                auto chunk = [&](const uint32_t (&r)[32], int c) {
                     const int n0 = nt * BN + c;
                     if (!row_ok || n0 >= p.N) return;
-                    if (EPI == kEpiFused) {
-                        uint16_t* yrow = reinterpret_cast<uint16_t*>(p.out) + (int64_t)row * p.f.ldy;
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            if (n0 + v * 8 < p.N)
-                                *reinterpret_cast<uint4*>(yrow + n0 + v * 8) =
-                                    epi_fused8(r + v * 8, sxr, sw_s + c + v * 8, bias_s + c + v * 8, q[v], p.f.act);
-                    } else if (EPI == kEpiMoeGated) {
+                    if (EPI == kEpiMoeGated) {
                         // columns n0 .. n0+31 of expert e: 16 (gate, up) pairs
                         float* arow = p.a_out + (int64_t)row * (p.N / 2) + n0 / 2;
 #pragma unroll
@@ -538,19 +510,13 @@ __global__ void __launch_bounds__(tc_threads<NEPI>(), 1)
                 if (c < BN) tmem_ld_32x32b_x32(tqa + (uint32_t)c, ra);
                 while (c < BN) {
                     tc_wait_ld();
-                    if (c + kStep < BN) {
-                        tmem_ld_32x32b_x32(tqa + (uint32_t)(c + kStep), rb);
-                        load_res(qb, c + kStep);
-                    }
-                    chunk(ra, qa, c);
+                    if (c + kStep < BN) tmem_ld_32x32b_x32(tqa + (uint32_t)(c + kStep), rb);
+                    chunk(ra, c);
                     c += kStep;
                     if (c >= BN) break;
                     tc_wait_ld();
-                    if (c + kStep < BN) {
-                        tmem_ld_32x32b_x32(tqa + (uint32_t)(c + kStep), ra);
-                        load_res(qa, c + kStep);
-                    }
-                    chunk(rb, qb, c);
+                    if (c + kStep < BN) tmem_ld_32x32b_x32(tqa + (uint32_t)(c + kStep), ra);
+                    chunk(rb, c);
                     c += kStep;
                 }
                 tc_fence_before();

@@ -13,6 +13,7 @@
 #include "attention.cuh"
 #include "common.cuh"
 #include "fwht.cuh"
+#include "gemm_split.cuh"
 #include "gemm_tc.cuh"
 #include "gemm_tc2.cuh"
 #include "gemv.cuh"
@@ -92,13 +93,12 @@ template <int BN, int STAGES, int EPI, int NACC, int NEPI = 4>
 int launch_tc(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st) {
     using SM = TcSmem<BN, STAGES>;
     auto kern = gemm_i8_tc_kernel<BN, STAGES, EPI, NACC, false, NEPI>;
-    constexpr int kBytes = EPI == kEpiFused ? SM::kBytesFused : SM::kBytes;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return W8A8_ERR_CUDA;
     static bool attr_done[kMaxDevices] = {false};
     if (dev >= kMaxDevices) return W8A8_ERR_UNSUPPORTED;
     if (!attr_done[dev]) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes) != cudaSuccess)
             return W8A8_ERR_CUDA;
         attr_done[dev] = true;
     }
@@ -110,7 +110,7 @@ int launch_tc(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st) {
     p.num_k_blocks = (p.K + kTcBK - 1) / kTcBK;
     const int tiles = p.num_m_tiles * p.num_n_tiles;
     const int grid = tiles < device_sms(dev) ? tiles : device_sms(dev);
-    kern<<<grid, tc_threads<NEPI>(), kBytes, st>>>(ta, tb, p);
+    kern<<<grid, tc_threads<NEPI>(), SM::kBytes, st>>>(ta, tb, p);
     return last_launch_status();
 }
 
@@ -244,15 +244,77 @@ int run_tc(const int8_t* qx, const float* sx, const int8_t* qw, const float* sw,
     p.out = out;
     if (epi == kEpiFused) {
         p.f = *fused;
-        if (M >= kTc2MinM) return launch_tc2<kEpiFused>(qx, qw, p, st);
-        return pick_bn(M, N, current_sms()) == 256 ? launch_tc<256, 4, kEpiFused, 2>(qx, qw, p, st)
-                                                   : launch_tc<128, 6, kEpiFused, 2>(qx, qw, p, st);
+        return launch_tc2<kEpiFused>(qx, qw, p, st);
     }
     if (M >= kTc2MinM) return epi == kEpiBf16 ? launch_tc2<kEpiBf16>(qx, qw, p, st) : launch_tc2<kEpiS32>(qx, qw, p, st);
     const int bn = pick_bn(M, N, current_sms());
     if (epi == kEpiBf16)
         return bn == 256 ? launch_tc<256, 4, kEpiBf16, 2>(qx, qw, p, st) : launch_tc<128, 6, kEpiBf16, 2>(qx, qw, p, st);
     return bn == 256 ? launch_tc<256, 4, kEpiS32, 2>(qx, qw, p, st) : launch_tc<128, 6, kEpiS32, 2>(qx, qw, p, st);
+}
+
+// Launch attribute: right after this library's activation-quant kernel (whose
+// inputs were complete before it started), the weight stream may begin while
+// that kernel finishes; codes, scales and counters are read only after it.
+// Otherwise plain stream order.
+void pdl_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* at, bool after_quant) {
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = after_quant ? 1 : 0;
+}
+
+// The epilogue linear between the GEMV and the pair tiles: weight tiles of 128
+// rows over clusters that share K (gemm_split.cuh), right after the quant.
+template <int BN>
+int launch_split(const int8_t* X, const int8_t* W, SpArgs a, int64_t K, cudaStream_t st) {
+    using SM = SpSmem<BN>;
+    auto kern = gemm_split_kernel<BN>;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return W8A8_ERR_CUDA;
+    if (dev < 0 || dev >= kMaxDevices) return W8A8_ERR_UNSUPPORTED;
+    static bool attr_done[kMaxDevices] = {false};
+    if (!attr_done[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes) != cudaSuccess)
+            return W8A8_ERR_CUDA;
+        attr_done[dev] = true;
+    }
+    CUtensorMap tw, tx;
+    if (!make_tmap_i8(&tw, W, (uint64_t)a.N, (uint64_t)K, 128)) return W8A8_ERR_CUDA;
+    if (!make_tmap_i8(&tx, X, (uint64_t)a.M, (uint64_t)K, BN)) return W8A8_ERR_CUDA;
+    a.nkb = (int)((K + kTcBK - 1) / kTcBK);
+    a.mtiles = (a.M + BN - 1) / BN;
+    const int64_t tiles = (int64_t)((a.N + 127) / 128) * a.mtiles;
+    // as many CTAs as the SMs' two slots hold, each with two k blocks at least
+    int S = 1;
+    while (S < 8 && tiles * (S + 1) <= 2 * device_sms(dev) && 2 * (S + 1) <= a.nkb) ++S;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * S), 1, 1);
+    cfg.blockDim = dim3(kSpThreads, 1, 1);
+    cfg.dynamicSmemBytes = SM::kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    pdl_config(cfg, at, true);
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)S;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kern, tw, tx, a));
+}
+
+int run_split(const int8_t* qx, const float* sx, const int8_t* qw, const float* sw, uint16_t* y, int64_t M, int64_t N,
+              int64_t K, const EpiFused& f, cudaStream_t st) {
+    SpArgs a = {};
+    a.sx = sx;
+    a.sw = sw;
+    a.y = y;
+    a.f = f;
+    a.M = (int)M;
+    a.N = (int)N;
+    return M <= 32 ? launch_split<32>(qx, qw, a, K, st)
+         : M <= 64 ? launch_split<64>(qx, qw, a, K, st)
+                   : launch_split<128>(qx, qw, a, K, st);
 }
 
 // ----------------------------------------------------------------- GEMV
@@ -328,17 +390,6 @@ size_t gemv_ws_bytes(const GemvPlan& g) { return g.part_bytes + align_up((size_t
 
 int* gemv_counters(const GemvPlan& g, void* scratch) {
     return g.counters ? reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(scratch) + g.part_bytes) : nullptr;
-}
-
-// Launch attribute: right after this library's activation-quant kernel (whose
-// inputs were complete before it started), the weight stream may begin while
-// that kernel finishes; codes, scales and counters are read only after it.
-// Otherwise plain stream order.
-void pdl_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* at, bool after_quant) {
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = after_quant ? 1 : 0;
 }
 
 template <int BN>
@@ -791,6 +842,7 @@ int w8a8_linear_epilogue(const uint16_t* x, int64_t ldx, const int8_t* qw, const
                                     true) != cudaSuccess)
         return W8A8_ERR_CUDA;
     if (gemv) return run_gemv(qx, sx, qw, sw, y, M, N, K, false, g, scratch, true, st, &f);
+    if (M < kTc2MinM) return run_split(qx, sx, qw, sw, y, M, N, K, f, st);
     return run_tc(qx, sx, qw, sw, y, M, N, K, kEpiFused, st, &f);
 }
 
