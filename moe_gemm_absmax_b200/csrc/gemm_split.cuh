@@ -155,10 +155,15 @@ __global__ void __launch_bounds__(kSpThreads, 2)
             if (lane < 2 && n0 + 64 * lane < a.N)
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(a.f.res + (int64_t)(m0 + i) * a.f.ldr + n0 + 64 * lane));
     }
+    const int n = n0 + 4 * lane;
+    float4 sw = make_float4(0.0f, 0.0f, 0.0f, 0.0f), bias = sw;
+    if (n < a.N) {
+        sw = __ldg(reinterpret_cast<const float4*>(a.sw + n));
+        if (a.f.bias) bias = __ldg(reinterpret_cast<const float4*>(a.f.bias + n));
+    }
     // the sums are complete, and with them every read of the ring
-    bool ok = true;
     if (warp >= 4) {
-        ok = mbar_wait_bounded(done, 0u, abort_flag, (kKernelIdSplit << 16) | 4);
+        const bool ok = mbar_wait_bounded(done, 0u, abort_flag, (kKernelIdSplit << 16) | 4);
         tc_fence_after();
         if (ok) {
             const int quarter = warp & 3, half = (warp - 4) >> 2;
@@ -180,29 +185,48 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     __syncthreads();      // the warps whose first lane had a role are whole again
     cluster_sync_all();   // every CTA's sums are in its shared memory
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int n = n0 + 4 * lane;
     if (n < a.N) {
-        const float4 sw = __ldg(reinterpret_cast<const float4*>(a.sw + n));
-        float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (a.f.bias) bias = __ldg(reinterpret_cast<const float4*>(a.f.bias + n));
         const uint32_t own = smem_u32(smem) + 16 * lane;
-        for (int i = (int)r + (int)S * warp; i < mv; i += (int)S * (kSpThreads / 32)) {
-            const int64_t row = m0 + i;
-            uint2 res = make_uint2(0, 0);
-            if (a.f.res) res = __ldcg(reinterpret_cast<const uint2*>(a.f.res + row * a.f.ldr + n));
-            const float sx = __ldcg(a.sx + row);
-            int4 acc = make_int4(0, 0, 0, 0);
-            for (uint32_t p = 0; p < S; ++p) {
-                int4 v;
-                asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                             : "r"(mapa_shared(own + (uint32_t)i * 512, p)));
-                acc.x += v.x;
-                acc.y += v.y;
-                acc.z += v.z;
-                acc.w += v.w;
+        constexpr int kWarps = kSpThreads / 32, U = 4;     // U tokens of a warp at a time
+        for (int i0 = (int)r + (int)S * warp; i0 < mv; i0 += (int)S * kWarps * U) {
+            uint2 res[U];
+            float sx[U];
+            int4 acc[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int i = i0 + (int)S * kWarps * j;
+                res[j] = make_uint2(0, 0);
+                acc[j] = make_int4(0, 0, 0, 0);
+                sx[j] = 0.0f;
+                if (i < mv) {
+                    if (a.f.res) res[j] = __ldcg(reinterpret_cast<const uint2*>(a.f.res + (int64_t)(m0 + i) * a.f.ldr + n));
+                    sx[j] = __ldcg(a.sx + m0 + i);
+                }
             }
-            *reinterpret_cast<uint2*>(a.y + row * a.f.ldy + n) = epi_fused4(acc, sx, sw, bias, res, a.f.act);
+            for (uint32_t p = 0; p < S; ++p) {
+                const uint32_t from = mapa_shared(own, p);
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const int i = i0 + (int)S * kWarps * j;
+                    if (i < mv) {
+                        int4 v;
+                        asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "r"(from + (uint32_t)i * 512));
+                        acc[j].x += v.x;
+                        acc[j].y += v.y;
+                        acc[j].z += v.z;
+                        acc[j].w += v.w;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int i = i0 + (int)S * kWarps * j;
+                if (i < mv)
+                    *reinterpret_cast<uint2*>(a.y + (int64_t)(m0 + i) * a.f.ldy + n) =
+                        epi_fused4(acc[j], sx[j], sw, bias, res[j], a.f.act);
+            }
         }
     }
     cluster_sync_all();   // no CTA leaves while another reads its sums

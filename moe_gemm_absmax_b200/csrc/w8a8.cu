@@ -285,9 +285,14 @@ int launch_split(const int8_t* X, const int8_t* W, SpArgs a, int64_t K, cudaStre
     a.nkb = (int)((K + kTcBK - 1) / kTcBK);
     a.mtiles = (a.M + BN - 1) / BN;
     const int64_t tiles = (int64_t)((a.N + 127) / 128) * a.mtiles;
-    // as many CTAs as the SMs' two slots hold, each with two k blocks at least
+    // CTAs that share a tile's K: as many as the SMs' two slots hold, each with
+    // two k blocks at least.  Powers of two, which fill the GPCs' slots (K =
+    // 17408, N = 5120, 16 tokens: 2 / 4 / 6 / 7 CTAs a tile 27.4 / 23.0 / 22.7 /
+    // 29.9 us); eight only where they get an SM each (N = 1024: 4 / 8 CTAs a
+    // tile 17.6 / 13.9 us, but K = 2048, N = 4096: 7.1 / 8.4 us)
+    const int sms = device_sms(dev);
     int S = 1;
-    while (S < 8 && tiles * (S + 1) <= 2 * device_sms(dev) && 2 * (S + 1) <= a.nkb) ++S;
+    while (S < 8 && tiles * 2 * S <= (S < 4 ? 2 * sms : sms) && 4 * S <= a.nkb) S *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * S), 1, 1);
     cfg.blockDim = dim3(kSpThreads, 1, 1);
@@ -301,6 +306,14 @@ int launch_split(const int8_t* X, const int8_t* W, SpArgs a, int64_t K, cudaStre
     at[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
     return cuda_status(cudaLaunchKernelEx(&cfg, kern, tw, tx, a));
+}
+
+// Where the split tiles serve: to 128 tokens, and as long as two CTAs can share
+// each of them (K = 17408, N = 5120: 384 tokens 46.1 us against the pair tiles'
+// 48.3, 512 tokens 72.6 against 50.1; K = 5120, N = 17408: 128 tokens 27.1
+// against about 30, 200 tokens 35.7 against 31.4).
+bool use_split(int64_t M, int64_t N) {
+    return M <= 128 || (M + 127) / 128 * ((N + 127) / 128) <= current_sms();
 }
 
 int run_split(const int8_t* qx, const float* sx, const int8_t* qw, const float* sw, uint16_t* y, int64_t M, int64_t N,
@@ -842,7 +855,7 @@ int w8a8_linear_epilogue(const uint16_t* x, int64_t ldx, const int8_t* qw, const
                                     true) != cudaSuccess)
         return W8A8_ERR_CUDA;
     if (gemv) return run_gemv(qx, sx, qw, sw, y, M, N, K, false, g, scratch, true, st, &f);
-    if (M < kTc2MinM) return run_split(qx, sx, qw, sw, y, M, N, K, f, st);
+    if (use_split(M, N)) return run_split(qx, sx, qw, sw, y, M, N, K, f, st);
     return run_tc(qx, sx, qw, sw, y, M, N, K, kEpiFused, st, &f);
 }
 
