@@ -518,53 +518,68 @@ ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
 
 def _placed(fn):
     """Runs fn with the device of its first tensor current and, where a stream is given, on that stream: what fn
-    allocates then belongs to the stream that uses it, so the caching allocator cannot hand it on too early."""
+    allocates then belongs to the stream that uses it, so the caching allocator cannot hand it on too early.  fn gets
+    the raw stream as its last argument."""
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kwargs):
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise TypeError(f"{fn.__name__}: the first argument must be a CUDA tensor")
+        index = first.device.index
         if stream is not None:
             if stream.device != first.device:
                 raise ValueError("stream is on another device than the tensors")
             with torch.cuda.stream(stream):
-                return fn(first, *args, **kwargs)
-        if first.device.index != torch.cuda.current_device():
-            with torch.cuda.device(first.device):
-                return fn(first, *args, **kwargs)
-        return fn(first, *args, **kwargs)
+                return fn(first, *args, raw_stream=stream.cuda_stream, **kwargs)
+        if index != torch.cuda.current_device():
+            with torch.cuda.device(index):
+                return fn(first, *args, raw_stream=_raw_stream(index), **kwargs)
+        return fn(first, *args, raw_stream=_raw_stream(index), **kwargs)
     return call
 
 
+def _raw_stream(index: int) -> int:
+    """cudaStream_t of the device's current stream, without a Stream object around it (3 us of a 10 us call)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _on(t, dtype, name, shape, device):
-    """Contiguous tensor of this type, shape and device."""
-    _need(t, dtype, name)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
+    """Contiguous tensor of this type, shape and device; its address."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != device \
+            or not t.is_contiguous():
+        _need(t, dtype, name)
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t.data_ptr()
 
 
 def _row_stride(t, dtype, name, device, shape=None, ndim=2) -> int:
     """Row stride of a tensor whose rows (all but the first dim) are dense."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise TypeError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != ndim or (shape is not None and t.shape != shape):
+    size = t.shape
+    if len(size) != ndim or (shape is not None and size != shape):
         raise ValueError(f"{name} must have shape {tuple(shape) if shape is not None else f'({ndim} dims)'}, "
-                         f"got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+                         f"got {tuple(size)}")
+    step = t.stride()
     n = 1
-    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and step != n:
+    for i in range(ndim - 1, 0, -1):
+        if step[i] != n and size[i] != 1:
             raise ValueError(f"{name}: all but the first dim must be dense")
-        n *= size
-    return t.stride(0) if t.shape[0] > 1 else n
+        n *= size[i]
+    return step[0] if size[0] > 1 else n
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_ws(M: int, N: int, K: int) -> int:
+    return max(linear_workspace_size(M, N, K), 256)
 
 
 @_placed
-def linear_epilogue(x, qw, sw, bias=None, act: int = ACT_NONE, residual=None, y=None, ws=None) -> torch.Tensor:
+def linear_epilogue(x, qw, sw, bias=None, act: int = ACT_NONE, residual=None, y=None, ws=None, *,
+                    raw_stream) -> torch.Tensor:
     """Online W8A8 linear with its epilogue: y = residual + act(linear(x) + bias), rounded to bf16 once.
 
     x bf16 [M,K]; qw int8 [N,K], sw fp32 [N]; bias fp32 [N]; residual and y bf16 [M,N].  x, residual and y may be
@@ -576,40 +591,40 @@ def linear_epilogue(x, qw, sw, bias=None, act: int = ACT_NONE, residual=None, y=
     if not isinstance(qw, torch.Tensor) or qw.dim() != 2:
         raise TypeError("qw must be a 2-D CUDA tensor")
     N = qw.shape[0]
-    _on(qw, torch.int8, "qw", (N, K), dev)
-    _on(sw, torch.float32, "sw", (N,), dev)
-    if bias is not None:
-        _on(bias, torch.float32, "bias", (N,), dev)
-    ldr = 0 if residual is None else _row_stride(residual, torch.bfloat16, "residual", dev, (M, N))
+    pw, ps = _on(qw, torch.int8, "qw", (N, K), dev), _on(sw, torch.float32, "sw", (N,), dev)
+    pb = None if bias is None else _on(bias, torch.float32, "bias", (N,), dev)
+    ldr, pr = 0, None
+    if residual is not None:
+        ldr, pr = _row_stride(residual, torch.bfloat16, "residual", dev, (M, N)), residual.data_ptr()
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    ldy = _row_stride(y, torch.bfloat16, "y", dev, (M, N))
+        y, ldy = x.new_empty((M, N)), N
+    else:
+        ldy = _row_stride(y, torch.bfloat16, "y", dev, (M, N))
     if ws is None:
-        ws = _workspace(linear_workspace_size(M, N, K), dev)
-    _check(lib().w8a8_linear_epilogue(_ptr(x), ldx, _ptr(qw), _ptr(sw), _ptr(bias), act, _ptr(residual), ldr, _ptr(y),
-                                      ldy, M, N, K, _ptr(ws), ws.numel(), _stream()), "w8a8_linear_epilogue")
+        ws = x.new_empty(_linear_ws(M, N, K), dtype=torch.uint8)
+    _check(lib().w8a8_linear_epilogue(x.data_ptr(), ldx, pw, ps, pb, act, pr, ldr, y.data_ptr(), ldy, M, N, K,
+                                      ws.data_ptr(), ws.numel(), raw_stream), "w8a8_linear_epilogue")
     return y
 
 
 # ------------------------------------------------------------------ paged cache and attention
 
 def _cache_args(k_cache, v_cache, k_scale, v_scale, device):
-    """(pages, Hkv, page size, D) of a paged cache: int8 with scales, or bf16 without."""
+    """Shape (pages, Hkv, page size, D) of a paged cache, int8 with scales or bf16 without, and its addresses."""
     dtype = torch.bfloat16 if k_scale is None else torch.int8
     _need(k_cache, dtype, "k_cache", 4)
     shape = k_cache.shape
-    _on(k_cache, dtype, "k_cache", shape, device)
-    _on(v_cache, dtype, "v_cache", shape, device)
-    if (k_scale is None) != (v_scale is None):
-        raise ValueError("k_scale and v_scale are given together or not at all")
-    if k_scale is not None:
-        _on(k_scale, torch.float32, "k_scale", shape[:3], device)
-        _on(v_scale, torch.float32, "v_scale", shape[:3], device)
-    return shape
+    pk, pv = _on(k_cache, dtype, "k_cache", shape, device), _on(v_cache, dtype, "v_cache", shape, device)
+    if k_scale is None:
+        if v_scale is not None:
+            raise ValueError("k_scale and v_scale are given together or not at all")
+        return shape, pk, pv, None, None
+    return (shape, pk, pv, _on(k_scale, torch.float32, "k_scale", shape[:3], device),
+            _on(v_scale, torch.float32, "v_scale", shape[:3], device))
 
 
 @_placed
-def kv_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None) -> None:
+def kv_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, *, raw_stream) -> None:
     """Writes the keys and values of T tokens into the paged cache, in place.
 
     k, v bf16 [T,Hkv,D] (token stride a multiple of 8, the rest dense); caches [pages,Hkv,page_size,D], int8 with
@@ -618,22 +633,27 @@ def kv_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None) -> None
     dev = k.device
     ldk = _row_stride(k, torch.bfloat16, "k", dev, ndim=3)
     ldv = _row_stride(v, torch.bfloat16, "v", dev, k.shape, ndim=3)
-    pages, Hkv, page, D = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
+    (pages, Hkv, page, D), pkc, pvc, pks, pvs = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
     T = k.shape[0]
     if k.shape[1:] != (Hkv, D):
         raise ValueError(f"k has heads {tuple(k.shape[1:])}, the cache {(Hkv, D)}")
-    _on(slots, torch.int64, "slots", (T,), dev)
-    _check(lib().w8a8_kv_append(_ptr(k), ldk, _ptr(v), ldv, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                _ptr(slots), T, Hkv, D, pages, page, _stream()), "w8a8_kv_append")
+    _check(lib().w8a8_kv_append(k.data_ptr(), ldk, v.data_ptr(), ldv, pkc, pvc, pks, pvs,
+                                _on(slots, torch.int64, "slots", (T,), dev), T, Hkv, D, pages, page, raw_stream),
+           "w8a8_kv_append")
 
 
 def paged_attention_workspace_size(B: int, Hq: int, Hkv: int, D: int) -> int:
     return int(lib().w8a8_paged_attention_workspace_size(B, Hq, Hkv, D))
 
 
+@functools.lru_cache(maxsize=1024)
+def _attention_ws(B: int, Hq: int, Hkv: int, D: int) -> int:
+    return max(paged_attention_workspace_size(B, Hq, Hkv, D), 256)
+
+
 @_placed
 def paged_attention(q, k_cache, v_cache, block_table, lengths, scale: float | None = None, k_scale=None, v_scale=None,
-                    y=None, ws=None) -> torch.Tensor:
+                    y=None, ws=None, *, raw_stream) -> torch.Tensor:
     """Attention of one new token per sequence over the paged cache -> bf16 [B,Hq,D].
 
     q bf16 [B,Hq,D] (sequence stride a multiple of 8, the rest dense); caches as in :func:`kv_append`; block_table
@@ -641,55 +661,59 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, scale: float | No
     length 0 gives zeros; absent pages and lengths past the table show in get_device_error()."""
     dev = q.device
     ldq = _row_stride(q, torch.bfloat16, "q", dev, ndim=3)
-    pages, Hkv, page, D = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
-    B, Hq, _ = q.shape
-    if q.shape[2] != D:
-        raise ValueError(f"q has head dim {q.shape[2]}, the cache {D}")
+    (pages, Hkv, page, D), pkc, pvc, pks, pvs = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
+    B, Hq, Dq = q.shape
+    if Dq != D:
+        raise ValueError(f"q has head dim {Dq}, the cache {D}")
     ld_table = _row_stride(block_table, torch.int32, "block_table", dev)
     if block_table.shape[0] != B:
         raise ValueError("block_table must have a row per sequence")
-    _on(lengths, torch.int32, "lengths", (B,), dev)
     if y is None:
-        y = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=dev)
-    _on(y, torch.bfloat16, "y", (B, Hq, D), dev)
+        y = q.new_empty((B, Hq, D))
+        py = y.data_ptr()
+    else:
+        py = _on(y, torch.bfloat16, "y", (B, Hq, D), dev)
     if ws is None:
-        ws = _workspace(paged_attention_workspace_size(B, Hq, Hkv, D), dev)
-    _check(lib().w8a8_paged_attention(_ptr(q), ldq, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                      _ptr(block_table), ld_table, _ptr(lengths), _ptr(y), B, Hq, Hkv, D, pages, page,
-                                      block_table.shape[1], D ** -0.5 if scale is None else scale, _ptr(ws),
-                                      ws.numel(), _stream()), "w8a8_paged_attention")
+        ws = q.new_empty(_attention_ws(B, Hq, Hkv, D), dtype=torch.uint8)
+    _check(lib().w8a8_paged_attention(q.data_ptr(), ldq, pkc, pvc, pks, pvs, block_table.data_ptr(), ld_table,
+                                      _on(lengths, torch.int32, "lengths", (B,), dev), py, B, Hq, Hkv, D, pages, page,
+                                      block_table.shape[1], D ** -0.5 if scale is None else scale, ws.data_ptr(),
+                                      ws.numel(), raw_stream), "w8a8_paged_attention")
     return y
 
 
 # ------------------------------------------------------------------ log probabilities
 
 @_placed
-def token_logprobs(logits, tokens=None, topk: int = 0, entropy: bool = True):
+def token_logprobs(logits, tokens=None, topk: int = 0, entropy: bool = True, *, raw_stream):
     """Log probabilities from the head's logits [M,V], bf16 or fp32 (rows may be strided).
 
     Returns (logprob, entropy, top_ids, top_logprobs): fp32 of the shape of tokens (int32 [M] or [M,G]; NaN for a
     token outside the vocabulary), fp32 [M] in nats, int32 [M,topk] by descending logit with ties to the lower index,
     fp32 [M,topk].  None for what was not asked for."""
-    dev = logits.device
-    if logits.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
-    ld = _row_stride(logits, logits.dtype, "logits", dev)
+    dev, dtype = logits.device, logits.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"logits must be torch.bfloat16 or torch.float32, got {dtype}")
+    ld = _row_stride(logits, dtype, "logits", dev)
     M, V = logits.shape
-    G, logprob, ids, top = 0, None, None, None
+    f32 = torch.float32
+    G, logprob, h, ids, top = 0, None, None, None, None
+    pt = pl = ph = pi = pv = None
     if tokens is not None:
-        _need(tokens, torch.int32, "tokens")
-        if tokens.dim() not in (1, 2) or tokens.shape[0] != M:
+        if not isinstance(tokens, torch.Tensor) or tokens.dim() not in (1, 2) or tokens.shape[0] != M:
             raise ValueError("tokens must be [M] or [M, G]")
-        _on(tokens, torch.int32, "tokens", tokens.shape, dev)
+        pt = _on(tokens, torch.int32, "tokens", tokens.shape, dev)
         G = 1 if tokens.dim() == 1 else tokens.shape[1]
-        logprob = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
-    h = torch.empty(M, dtype=torch.float32, device=dev) if entropy else None
+        logprob = logits.new_empty(tokens.shape, dtype=f32)
+        pl = logprob.data_ptr()
+    if entropy:
+        h = logits.new_empty(M, dtype=f32)
+        ph = h.data_ptr()
     if topk > 0:
-        ids = torch.empty((M, topk), dtype=torch.int32, device=dev)
-        top = torch.empty((M, topk), dtype=torch.float32, device=dev)
-    _check(lib().w8a8_token_logprobs(_ptr(logits), int(logits.dtype == torch.float32), ld, _ptr(tokens), G,
-                                     _ptr(logprob), _ptr(h), _ptr(ids), _ptr(top), M, V, topk, _stream()),
-           "w8a8_token_logprobs")
+        ids, top = logits.new_empty((M, topk), dtype=torch.int32), logits.new_empty((M, topk), dtype=f32)
+        pi, pv = ids.data_ptr(), top.data_ptr()
+    _check(lib().w8a8_token_logprobs(logits.data_ptr(), int(dtype is f32), ld, pt, G, pl, ph, pi, pv, M, V, topk,
+                                     raw_stream), "w8a8_token_logprobs")
     return logprob, h, ids, top
 
 
