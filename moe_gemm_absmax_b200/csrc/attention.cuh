@@ -230,6 +230,9 @@ __device__ __forceinline__ float attn_ex2(float x) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -300,6 +303,17 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
     int64_t before = place.before;
     const int pmask = (1 << a.page_shift) - 1;
     bool bad = false;
+    // this lane's places in a stage, per copy instruction of 32 units (they repeat every kDst)
+    constexpr int kDst = U == 8 ? 2 : (U >= 16 ? 8 * U / 32 : 1);
+    uint32_t kdst[kDst], vdst[kDst];
+#pragma unroll
+    for (int x = 0; x < kDst; ++x) {
+        const int r = (x * 32 + lane) / U, un = (x * 32 + lane) % U;
+        kdst[x] = (r * U + (U == 4 ? un : un ^ ((r & 1) << 2))) * 16;
+        vdst[x] = TT * ROW + (r * U + (U == 4 ? un : un ^ (((r >> 1) & 3) << 1))) * 16;
+    }
+    const uint8_t* kc_lane = reinterpret_cast<const uint8_t*>(a.kc) + 16 * lane;
+    const uint8_t* vc_lane = reinterpret_cast<const uint8_t*>(a.vc) + 16 * lane;
 
     while (u < u1) {
         const int64_t len = attn_len(a, b);
@@ -334,41 +348,45 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
         // after the other.  In shared memory a key row's units are XORed with 4
         // on odd rows and a value row's with 2 * (row / 2 % 4), which keeps both
         // reads below (8 rows x 4 units; 4 even or odd rows x 2 units) free of
-        // bank conflicts.
+        // bank conflicts.  Each lane finds its token's row; the rest is one
+        // 64-bit addition per eight tokens and constants.
         auto issue = [&](int pages, int64_t tile, int stage) {
-            const uint32_t ks = ring + stage * Cfg::kStage, vs = ks + TT * ROW, cs = vs + TT * ROW;
-            int64_t row0[NT8];
-            int here[NT8];
+            const uint32_t ks = ring + stage * Cfg::kStage;
+            const int64_t t0 = tile * TT;
+            const int64_t row = pages < 0 ? 0 : (((int64_t)pages * a.Hkv + h) << a.page_shift) + (((int)t0 + lane) & pmask);
+            const uint64_t off = (uint64_t)row * ROW;
+            const uint32_t off_lo = (uint32_t)off, off_hi = (uint32_t)(off >> 32);
+            const bool full = __all_sync(0xffffffffu, pages >= 0 || lane >= TT);
 #pragma unroll
             for (int j = 0; j < NT8; ++j) {
-                const int pg = __shfl_sync(0xffffffffu, pages, 8 * j);
-                const int64_t t = tile * TT + 8 * j;
-                here[j] = pg < 0 ? 0 : (int)(len - t < 8 ? len - t : 8);
-                row0[j] = pg < 0 ? 0 : (((int64_t)pg * a.Hkv + h) << a.page_shift) + ((int)t & pmask);
-                const uint8_t* ksrc = reinterpret_cast<const uint8_t*>(a.kc) + row0[j] * ROW + 16 * lane;
-                const uint8_t* vsrc = reinterpret_cast<const uint8_t*>(a.vc) + row0[j] * ROW + 16 * lane;
+                const uint64_t from = ((uint64_t)__shfl_sync(0xffffffffu, off_hi, 8 * j) << 32) | __shfl_sync(0xffffffffu, off_lo, 8 * j);
+                const uint8_t* ksrc = kc_lane + from;
+                const uint8_t* vsrc = vc_lane + from;
+                if (full) {
 #pragma unroll
-                for (int x = 0; x < U / 4; ++x) {
-                    const int r = (x * 32 + lane) / U, un = (x * 32 + lane) % U;
-                    const uint32_t n = r < here[j] ? 16u : 0u;
-                    const int ku = U == 4 ? un : un ^ ((r & 1) << 2), vu = U == 4 ? un : un ^ (((r >> 1) & 3) << 1);
-                    cp_async16(ks + ((8 * j + r) * U + ku) * 16, ksrc + 512 * x, n);
-                    cp_async16(vs + ((8 * j + r) * U + vu) * 16, vsrc + 512 * x, n);
+                    for (int x = 0; x < U / 4; ++x) {
+                        cp_async16(ks + kdst[x % kDst] + (8 * j * U + 32 * (x - x % kDst)) * 16, ksrc + 512 * x);
+                        cp_async16(ks + vdst[x % kDst] + (8 * j * U + 32 * (x - x % kDst)) * 16, vsrc + 512 * x);
+                    }
+                } else {
+                    const int here = __shfl_sync(0xffffffffu, pages, 8 * j) < 0 ? 0 : (int)(len - t0 - 8 * j < 8 ? len - t0 - 8 * j : 8);
+#pragma unroll
+                    for (int x = 0; x < U / 4; ++x) {
+                        const uint32_t n = (x * 32 + lane) / U < here ? 16u : 0u;
+                        cp_async16(ks + kdst[x % kDst] + (8 * j * U + 32 * (x - x % kDst)) * 16, ksrc + 512 * x, n);
+                        cp_async16(ks + vdst[x % kDst] + (8 * j * U + 32 * (x - x % kDst)) * 16, vsrc + 512 * x, n);
+                    }
                 }
             }
-            if (INT8 && lane < 4 * NT8) {
+            if (INT8) {
                 // lanes [0, 2 NT8): keys' scales, four tokens each; then values'
-                const int j = (lane >> 1) % NT8, half = lane & 1;
-                int64_t row = row0[0];
-                int n = here[0];
-#pragma unroll
-                for (int i = 1; i < NT8; ++i)
-                    if (j == i) {
-                        row = row0[i];
-                        n = here[i];
-                    }
-                const int left = min(max(n - 4 * half, 0), 4);
-                cp_async16(cs + lane * 16, (lane < 2 * NT8 ? a.ks : a.vs) + row + 4 * half, 4u * left);
+                const int tok = (lane * 4) % TT;
+                const uint64_t from = ((uint64_t)__shfl_sync(0xffffffffu, (uint32_t)(row >> 32), tok) << 32) |
+                                      __shfl_sync(0xffffffffu, (uint32_t)row, tok);
+                const int64_t left = __shfl_sync(0xffffffffu, pages, tok) < 0 ? 0 : len - t0 - tok;
+                if (lane < 4 * NT8)
+                    cp_async16(ks + 2 * TT * ROW + lane * 16, (lane < 2 * NT8 ? a.ks : a.vs) + from,
+                               left >= 4 ? 16u : 4u * (uint32_t)left);
             }
         };
         int64_t tile = ch0 * kAttnWarps + warp;
@@ -481,8 +499,8 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                 for (int j = 0; j < NT8; ++j)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        hi[0][j][k] = lo[0][j][k] = 0;
-                        if (NQ == 2) mid[j % (NQ == 2 ? NT8 : 1)][k] = 0;
+                        hi[0][j][k] = lo[0][j][k] = 0x4B400000;   // the bits of 1.5 * 2^23: sums come out as floats
+                        if (NQ == 2) mid[j % (NQ == 2 ? NT8 : 1)][k] = 0x4B400000;
                     }
 #pragma unroll
                 for (int i = 0; i < KL; ++i) {
@@ -516,7 +534,8 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                         }
                     }
                 }
-                // planes join: |sums| < 2^22, exact in fp32
+                // planes join: |sums| < 2^22, so sum + 1.5 * 2^23 is exact in fp32 and its bits were added up
+                auto value = [](int bits) { return __fsub_rn(__int_as_float(bits), 12582912.0f); };
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -526,8 +545,7 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                             const int p0 = hi[0][j][2 * n + e];
                             const int p1 = NQ == 1 ? hi[0][j][2 + e] : mid[j % (NQ == 2 ? NT8 : 1)][2 * n + e];
                             const int p2 = lo[0][j][2 * n + e];
-                            s[n][j][e] = __fmaf_rn(16384.0f, __int2float_rn(p0),
-                                                   __fmaf_rn(128.0f, __int2float_rn(p1), __int2float_rn(p2)));
+                            s[n][j][e] = __fmaf_rn(16384.0f, value(p0), __fmaf_rn(128.0f, value(p1), value(p2)));
                         }
             } else {
                 float acc[NT8][4];
@@ -591,10 +609,18 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                     for (int e = 0; e < 2; ++e) {
                         float v = s[n][j][e] * qscale[n];
                         if (INT8) v *= e ? ksc[j].y : ksc[j].x;
-                        x[j][e] = (there >> (8 * j + 2 * c + e)) & 1u ? v : -INFINITY;
-                        mx = fmaxf(mx, x[j][e]);
+                        x[j][e] = v;
                     }
                 }
+                if (there != 0xffffffffu) {
+#pragma unroll
+                    for (int j = 0; j < NT8; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (!((there >> (8 * j + 2 * c + e)) & 1u)) x[j][e] = -INFINITY;
+                }
+#pragma unroll
+                for (int j = 0; j < NT8; ++j) mx = fmaxf(mx, fmaxf(x[j][0], x[j][1]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const float mn = fmaxf(m[n], mx);
