@@ -234,6 +234,19 @@ template <int WN, int WK, int TG, int U, int MINB = 1, bool FUSED = false>
 __global__ void __launch_bounds__(kGemvThreads, MINB) gemv_dense_kernel(GemvShape a, GemvEpiDense e) {
     int acc[TG][4];
     int block;
+    if (FUSED && threadIdx.x < 32 * WN) {
+        // what the epilogue will want, on its way to L2 while the weights stream
+        // (all of it older than the activation quant): lanes 0..7 a residual row
+        // each, then scales and biases
+        const int l = threadIdx.x & 31, n0 = (blockIdx.x * WN + (threadIdx.x >> 5)) * 16;
+        const void* p = nullptr;
+        if (n0 < e.N) {
+            if (l < e.M && l < 8 && e.f.res) p = e.f.res + l * e.f.ldr + n0;
+            if (l == 8) p = e.sw + n0;
+            if (l == 9 && e.f.bias) p = e.f.bias + n0;
+        }
+        if (p) asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+    }
     if (!gemv_core<WN, WK, TG, RowMapDense, U>(a, acc, block, blockIdx.y, gridDim.y, blockIdx.x)) return;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
