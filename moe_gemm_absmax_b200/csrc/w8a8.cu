@@ -308,12 +308,17 @@ int launch_split(const int8_t* X, const int8_t* W, SpArgs a, int64_t K, cudaStre
     return cuda_status(cudaLaunchKernelEx(&cfg, kern, tw, tx, a));
 }
 
-// Where the split tiles serve: to 128 tokens, and as long as two CTAs can share
-// each of them (K = 17408, N = 5120: 384 tokens 46.1 us against the pair tiles'
-// 48.3, 512 tokens 72.6 against 50.1; K = 5120, N = 17408: 128 tokens 27.1
-// against about 30, 200 tokens 35.7 against 31.4).
-bool use_split(int64_t M, int64_t N) {
-    return M <= 128 || (M + 127) / 128 * ((N + 127) / 128) <= current_sms();
+// Which kernel the epilogue linear takes: 0 the GEMV, 1 split tiles, 2 pair tiles.
+// To 4 tokens the GEMV (K = 5120, N = 5120: 7.9 - 9.0 us against 9.2 - 9.7), to 8
+// where the weights are not much longer than wide (K = 2048, N = 4096: 6.5
+// against 6.8; but K = 17408, N = 5120: 22.7 against 21.1).  Split tiles to 128
+// tokens, and on as long as two CTAs can share each of them (K = 17408, N = 5120:
+// 384 tokens 46.1 us against the pair tiles' 48.3, 512 tokens 72.6 against 50.1;
+// K = 5120, N = 17408: 128 tokens 27.1 against about 30, 200 tokens 35.7 against
+// 31.4).
+int epilogue_path(int64_t M, int64_t N, int64_t K) {
+    if (M <= 4 || (M <= 8 && K <= 2 * N)) return 0;
+    return M <= 128 || (M + 127) / 128 * ((N + 127) / 128) <= current_sms() ? 1 : 2;
 }
 
 int run_split(const int8_t* qx, const float* sx, const int8_t* qw, const float* sw, uint16_t* y, int64_t M, int64_t N,
@@ -842,7 +847,8 @@ int w8a8_linear_epilogue(const uint16_t* x, int64_t ldx, const int8_t* qw, const
     int8_t* qx = reinterpret_cast<int8_t*>(ws);
     float* sx = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + align_up((size_t)M * K, 256));
     void* scratch = reinterpret_cast<uint8_t*>(sx) + align_up((size_t)M * 4, 256);
-    const bool gemv = M <= 8;
+    const int path = epilogue_path(M, N, K);
+    const bool gemv = path == 0;
     GemvPlan g = gemv_plan(M, N, K);
     int* ctr = gemv ? gemv_counters(g, scratch) : nullptr;
     EpiFused f;
@@ -855,7 +861,7 @@ int w8a8_linear_epilogue(const uint16_t* x, int64_t ldx, const int8_t* qw, const
                                     true) != cudaSuccess)
         return W8A8_ERR_CUDA;
     if (gemv) return run_gemv(qx, sx, qw, sw, y, M, N, K, false, g, scratch, true, st, &f);
-    if (use_split(M, N)) return run_split(qx, sx, qw, sw, y, M, N, K, f, st);
+    if (path == 1) return run_split(qx, sx, qw, sw, y, M, N, K, f, st);
     return run_tc(qx, sx, qw, sw, y, M, N, K, kEpiFused, st, &f);
 }
 
@@ -1662,7 +1668,7 @@ int launch_attn_nq(const AttnArgs& a, cudaStream_t st) {
 
 template <int D, bool INT8>
 int launch_append(const KvAppendArgs& a, cudaStream_t st) {
-    constexpr int kRows = 256 / (D / 16);   // a CTA's
+    constexpr int kRows = 256 / AppendCfg<D, INT8>::L;   // a CTA's
     kv_append_kernel<D, INT8><<<dim3((unsigned)((a.T * a.Hkv + kRows - 1) / kRows), 1, 1), 256, 0, st>>>(a);
     return last_launch_status();
 }

@@ -156,6 +156,34 @@ def test_attention_pages_and_lengths(page, int8):
 
 
 @pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("D,G", [(64, 9), (256, 3), (256, 10)])
+def test_attention_small_pages_of_other_heads(D, G, int8):
+    c = Cache([5, 8, 0, 71, 64, 200], 3, D, 8, int8, seed=D)
+    q = _q(6, 3 * G, D)
+    _check(c, q, c.attend(q))
+
+
+@pytest.mark.parametrize("int8", [True, False])
+def test_attention_nan_stays_in_its_head(int8):
+    """A NaN in one query head, and one in one key, reach the outputs that use them and no others."""
+    c = Cache([100, 100], 2, 128, 16, int8)
+    q = _q(2, 8, 128)
+    want = c.attend(q)
+    q[0, 1, 5] = math.nan
+    q[0, 6, 7] = math.inf
+    if int8:
+        c.ks[c.table[1, 2].long(), 1, 3] = math.nan
+    else:
+        c.k[c.table[1, 2].long(), 1, 3, 9] = math.nan
+    y = c.attend(q)
+    hurt = torch.zeros((2, 8), dtype=torch.bool, device="cuda")
+    hurt[0, 1] = hurt[0, 6] = True
+    hurt[1, 4:] = True
+    assert torch.equal(torch.isnan(y).all(dim=2), hurt) and torch.equal(y[~hurt], want[~hurt])
+    assert w8a8.get_device_error() == (w8a8.OK, 0)
+
+
+@pytest.mark.parametrize("int8", [True, False])
 @pytest.mark.parametrize("D,Hkv,G,lens", [(128, 8, 4, [3001]), (128, 1, 8, [20000, 5]), (256, 4, 6, [2500, 1, 900]),
                                           (64, 2, 16, [9999]), (128, 2, 12, [1500, 4000])])
 def test_attention_long(D, Hkv, G, lens, int8):

@@ -75,6 +75,18 @@ def test_epilogue_small(M, K, N, name):
     assert w8a8.get_device_error() == (w8a8.OK, 0)
 
 
+@pytest.mark.parametrize("M,K,N", [(1, 16, 8), (8, 16, 8), (9, 16, 8), (33, 144, 8), (129, 16, 136), (700, 32, 24),
+                                   # clusters of 2, 4 and 8 along K, uneven shares of its blocks
+                                   (5, 2064, 200), (16, 9232, 1024), (40, 4112, 512), (200, 1296, 5120), (7, 17408, 264),
+                                   # more tiles than SMs
+                                   (128, 256, 40000), (260, 400, 20000)])
+def test_epilogue_shapes(M, K, N):
+    x, qw, sw, bias, res = _case(M, K, N, 11)
+    _check(w8a8.linear_epilogue(x, qw, sw, bias=bias, residual=res), x, qw, sw, bias, res, "none")
+    _check(w8a8.linear_epilogue(x, qw, sw, bias=bias, act=w8a8.ACT_GELU), x, qw, sw, bias, None, "gelu")
+    assert w8a8.get_device_error() == (w8a8.OK, 0)
+
+
 @pytest.mark.parametrize("M", [1, 8, 16, 32, 100, 512])
 def test_epilogue_none_is_the_linear(M):
     x, qw, sw, _, _ = _case(M, 1024, 512, M)
