@@ -350,7 +350,7 @@ W8A8_API int w8a8_moe_g128_forward(const uint16_t* x, const uint16_t* logits, co
  *   v[m,n] = (float(sum_k qx[m,k] qw[n,k]) * sx[m]) * sw[n]   as w8a8_linear
  *   y[m,n] = bf16_rne( residual[m,n] + act( v[m,n] + bias[n] ) )
  * with one fp32 rounding for each product and sum; the activations are in
- * fp32 (SILU and GELU_TANH within 2^-20 of their value, GELU = v * Phi(v)).
+ * fp32, within 2^-18 of their value (beyond |v| = 80 they are 0 or v).
  * Strides are in elements and multiples of 8 (ldx >= K, ldr >= N, ldy >= N);
  * elements of y between N and ldy are not touched.  y may be the residual
  * itself (same pointer and stride: the residual stream updated in place); it
@@ -367,7 +367,8 @@ W8A8_API int w8a8_linear_epilogue(const uint16_t* x, int64_t ldx, const int8_t* 
 
 /* ---------------------------------------------------------------------------
  * The paged key-value cache of the attention layers -- [IQ8R] (int8 cache with
- * one scale per token and head) and [ATOM] "Precision split" (cache in bf16).
+ * one scale per token and head; fp32 here, the type of this library's other
+ * per-token scales) and [ATOM] "Precision split" (cache in bf16).
  *   k_cache, v_cache  [num_pages, Hkv, page_size, D], int8 or bf16
  *   k_scale, v_scale  fp32 [num_pages, Hkv, page_size] for int8 (a value is
  *                     float(code) * scale); both NULL for bf16
@@ -394,15 +395,21 @@ W8A8_API int w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, i
  *      page_size positions; only the first ceil(length / page_size) entries
  *      of a row are read
  *   lengths  int32 [B]: positions that the token attends to, itself included
- *   y  bf16 [B, Hq, D], dense
+ *   y  bf16 [B, Hq, D], dense; may not overlap the inputs
  *   l_t = scale * (q . k_t),  p_t = exp(l_t - max l),
  *   y = bf16_rne( sum_t p_t v_t / sum_t p_t )   for t < lengths[b]
- * Scores, maxima, sums and outputs are held in fp32.  A sequence of length 0
+ * Scores, maxima, sums and outputs are held in fp32; int8 codes meet the query
+ * as integers (its head scaled by a power of two to 21 bits), probabilities
+ * times value scales round to fp16 (2^-11) below that, with a bf16 cache to two
+ * bf16 (2^-16).  A NaN or infinity in a query head, or in a key or value that is
+ * attended to, makes the outputs that it reaches NaN or infinite; what lies in
+ * the cache beyond a sequence's length is never used.  A sequence of length 0
  * (or less) gives zeros.  A length beyond max_pages * page_size is cut there,
  * and positions of a page number outside [0, num_pages) count as absent;
  * either records W8A8_ERR_INVALID_ARG in the device error word.
  * The context is split over the GPU and its parts are joined in a fixed order:
- * the same call gives the same bits again.  1 <= B <= 4096.
+ * the same call gives the same bits again.  1 <= B <= 4096.  `ws` belongs to one
+ * call at a time: calls that overlap on the GPU need workspaces of their own.
  * ws_bytes >= w8a8_paged_attention_workspace_size(B, Hq, Hkv, D). */
 W8A8_API size_t w8a8_paged_attention_workspace_size(int64_t B, int Hq, int Hkv, int D);
 W8A8_API int w8a8_paged_attention(const uint16_t* q, int64_t ldq, const void* k_cache, const void* v_cache,

@@ -52,7 +52,7 @@ __device__ __forceinline__ uint64_t f2_sigmoid(uint64_t mt) { return f2_rcp(f2_a
 __device__ __forceinline__ uint64_t act_relu(uint64_t v) {
     float a, b;
     f2_unpack(v, a, b);
-    return f2_pack(fmaxf(a, 0.0f), fmaxf(b, 0.0f));
+    return f2_pack(fmax_nan(a, 0.0f), fmax_nan(b, 0.0f));   // NaN stays NaN
 }
 __device__ __forceinline__ uint64_t act_silu(uint64_t v) {
     return f2_mul(v, f2_sigmoid(f2_mul(v, f2_const(-1.4426950408889634f))));

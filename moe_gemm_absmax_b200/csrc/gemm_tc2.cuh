@@ -183,6 +183,8 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
     if (warp == 0) {
         // ------------------------------------------------------------ producer (both CTAs)
         if (lane == 0) {
+            // kEpiFused is launched while the activation quant still runs
+            if (EPI == kEpiFused) asm volatile("griddepcontrol.wait;" ::: "memory");
             int stage = 0;
             uint32_t phase = 0, issued = 0, last_phase = 0;
             bool ok = true;
@@ -269,6 +271,7 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
         // ------------------------------------------------------------ epilogue (both CTAs)
         const int quarter = warp & 3;              // TMEM lanes [32 q, 32 q + 32)
         const int chalf = (warp - 2) >> 2;         // chunks c = 32 chalf + 64 i
+        if (EPI == kEpiFused) asm volatile("griddepcontrol.wait;" ::: "memory");
         const uint32_t tempty_leader0 = mapa_shared(smem_u32(&tempty[0]), 0);
         float* sw_s = epi_scratch + (warp - 2) * (SM::kEpiWarp / 4);   // this warp's copy of the tile's column scales
         int acc = 0;
@@ -278,7 +281,8 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
             const int row = mt * kTc2BM + (int)rank * 128 + quarter * 32 + lane;
             const bool row_ok = row < p.M;
             float sxr = 0.0f;
-            if ((EPI == kEpiBf16 || EPI == kEpiMoeGated || EPI == kEpiFused) && row_ok) sxr = __ldg(p.sx + row);
+            if ((EPI == kEpiBf16 || EPI == kEpiMoeGated) && row_ok) sxr = __ldg(p.sx + row);
+            if (EPI == kEpiFused && row_ok) sxr = __ldcg(p.sx + row);   // written by the kernel that it waited for
             if (EPI == kEpiBf16 || EPI == kEpiMoeGated) {
                 // the tile's BN column scales (N % 8 == 0: a 4-column vector is all in or all out)
                 __syncwarp();   // the previous tile's reads are done

@@ -127,7 +127,7 @@ int launch_tc2_bn(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st)
     cfg.blockDim = dim3(kTc2Threads, 1, 1);
     cfg.dynamicSmemBytes = SM::kBytes;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = 2;
     at[0].val.clusterDim.y = 1;
@@ -151,6 +151,11 @@ int launch_tc2_bn(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st)
     const int tiles = p.num_m_tiles * p.num_n_tiles;
     const int clusters = tiles < max_clusters[dev] ? tiles : max_clusters[dev];
     cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
+    if (EPI == kEpiFused) {   // set up while the activation quant before it finishes
+        at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 2;
+    }
     return cuda_status(cudaLaunchKernelEx(&cfg, kern, ta, tb, p));
 }
 

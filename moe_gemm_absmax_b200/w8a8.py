@@ -524,16 +524,16 @@ def _placed(fn):
     def call(first, *args, stream=None, **kwargs):
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise TypeError(f"{fn.__name__}: the first argument must be a CUDA tensor")
-        index = first.device.index
-        if stream is not None:
-            if stream.device != first.device:
-                raise ValueError("stream is on another device than the tensors")
-            with torch.cuda.stream(stream):
-                return fn(first, *args, raw_stream=stream.cuda_stream, **kwargs)
-        if index != torch.cuda.current_device():
+        index = first.get_device()
+        if stream is None and index == torch._C._cuda_getDevice():
+            return fn(first, *args, raw_stream=_raw_stream(index), **kwargs)
+        if stream is None:
             with torch.cuda.device(index):
                 return fn(first, *args, raw_stream=_raw_stream(index), **kwargs)
-        return fn(first, *args, raw_stream=_raw_stream(index), **kwargs)
+        if stream.device != first.device:
+            raise ValueError("stream is on another device than the tensors")
+        with torch.cuda.stream(stream):
+            return fn(first, *args, raw_stream=stream.cuda_stream, **kwargs)
     return call
 
 

@@ -119,6 +119,18 @@ def test_append(D, page, int8):
     assert bool((held == 77).all()) if int8 else bool(torch.isnan(held).all())
 
 
+def test_append_non_finite_rows_follow_the_quantizer():
+    k = torch.randn((6, 1, 128), generator=_gen(3), device="cuda").to(torch.bfloat16)
+    v = torch.randn((6, 1, 128), generator=_gen(4), device="cuda").to(torch.bfloat16)
+    k[0, 0, 7], k[1, 0, :], v[2, 0, 100] = math.nan, math.nan, math.inf
+    kc, vc = (torch.zeros((1, 1, 8, 128), dtype=torch.int8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((1, 1, 8), device="cuda") for _ in range(2))
+    w8a8.kv_append(k, v, kc, vc, torch.arange(6, device="cuda"), k_scale=ks, v_scale=vs)
+    for x, c, sc in ((k, kc, ks), (v, vc, vs)):
+        q, s = w8a8.quant_act(x.view(6, 128))
+        assert torch.equal(c[0, 0, :6], q) and torch.equal(sc[0, 0, :6], s)
+
+
 def test_append_strided_skipped_and_outside():
     Hkv, D, page, pages = 2, 128, 16, 4
     qkv = torch.randn((5, 8 * D), generator=_gen(0), device="cuda").to(torch.bfloat16)

@@ -115,6 +115,29 @@ def test_epilogue_strided_and_in_place(M):
     assert bool((wide_r[:, :8] == 5).all()) and bool((wide_r[:, 8 + N:] == 5).all())
 
 
+@pytest.mark.parametrize("M", [3, 8, 30, 130, 600])
+def test_epilogue_leaves_the_rows_behind(M):
+    """A padded batch: rows past M of input, residual and output are neither used nor written."""
+    K, N = 256, 136
+    x, qw, sw, bias, res = _case(M + 9, K, N, M)
+    x[M:], res[M:] = float("nan"), float("nan")
+    y = torch.full((M + 9, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    w8a8.linear_epilogue(x[:M], qw, sw, bias, w8a8.ACT_NONE, res[:M], y=y[:M])
+    _check(y[:M], x[:M], qw, sw, bias, res[:M], "none")
+    assert bool((y[M:] == 7).all())
+
+
+def test_epilogue_non_finite_residual_and_bias():
+    for M in (4, 20, 300):
+        x, qw, sw, bias, res = _case(M, 256, 64, M)
+        bias[3], res[1, 5], res[2, 6] = float("nan"), float("inf"), float("nan")
+        for name in ("none", "relu", "silu", "gelu", "gelu_tanh"):
+            y = w8a8.linear_epilogue(x, qw, sw, bias, ACTS[name], res)
+            nan = torch.zeros_like(y, dtype=torch.bool)
+            nan[:, 3], nan[2, 6] = True, True
+            assert torch.equal(torch.isnan(y), nan) and y[1, 5] == float("inf")
+
+
 def test_epilogue_extreme_values():
     """Zero rows, and pre-activations far out on both sides."""
     M, K, N = 6, 256, 64
