@@ -1647,7 +1647,40 @@ int launch_attn(AttnArgs a, cudaStream_t st) {
         attr_done[dev] = true;
     }
     const int64_t heads = (int64_t)a.Hkv * a.qtiles;
-    const int64_t most = (int64_t)a.B * heads * ((a.cap + Cfg::CH - 1) / Cfg::CH);   // chunks, if every sequence were full
+    const int64_t chunks = (a.cap + Cfg::CH - 1) / Cfg::CH;   // of a full sequence
+    // Clusters with a unit each, where that leaves a CTA few chunks; how few, goes
+    // by how much of the GPU they fill (shares would fill all of it, but pay for
+    // the search and the join).  8 heads of 128, int8, shares / clusters: 4
+    // sequences of up to 1000 9.6 / 8.5 us, of 4000 15.0 / 13.0; 16 of 2000 (8
+    // chunks a CTA) 21.6 / 19.4, of 4000 (16) 27.3 / 33.2; 64 of 1000 (8 chunks,
+    // one CTA a unit) 37.3 / 32.1, 256 of 2000 (16) 133 / 127.  Where a CTA fills an
+    // SM (D = 256, bf16), clusters of 8 do not pack (4 sequences of 500: 9.7 / 13.7
+    // us, by fours 9.2), and many units a CTA wait for one another's first loads
+    // (256 of 1000: 123 / 133).
+    const int64_t slots = (int64_t)kAttnSms * Cfg::kMinB;
+    const int64_t units = a.B * heads;
+    int C = 8;
+    while (C > 1 && (C / 2 >= chunks || units * C > (Cfg::kMinB == 1 && C == 8 ? slots * 3 / 4 : slots))) C /= 2;
+    const bool waits = Cfg::kMinB == 1 && units > 2 * slots;
+    const int64_t few = waits ? 4 : (units * C >= slots ? 16 : (units * C * 2 >= slots ? 8 : 4));
+    if (chunks <= few * C) {
+        a.csize = C;
+        a.grid = (int)(units * C);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)a.grid, 1, 1);
+        cfg.blockDim = dim3(kAttnThreads, 1, 1);
+        cfg.dynamicSmemBytes = Cfg::kBytes;
+        cfg.stream = st;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)C;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        return cuda_status(cudaLaunchKernelEx(&cfg, kern, a));
+    }
+    const int64_t most = units * chunks;                      // chunks, if every sequence were full
     a.grid = (int)(most < kAttnSms * Cfg::kMinB ? most : kAttnSms * Cfg::kMinB);
     kern<<<(unsigned)a.grid, kAttnThreads, Cfg::kBytes, st>>>(a);
     int rc = last_launch_status();
@@ -1656,9 +1689,9 @@ int launch_attn(AttnArgs a, cudaStream_t st) {
     // more threads share the parts (down to a warp's worth of outputs a CTA)
     constexpr int kItems = 8 * NQ * D / 4;
     int per_cta = kItems < kAttnJoinThreads ? kItems : kAttnJoinThreads;
-    while (per_cta > 32 && a.B * heads * (kItems / per_cta) < 4 * kAttnSms) per_cta /= 2;
+    while (per_cta > 32 && units * (kItems / per_cta) < 4 * kAttnSms) per_cta /= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.B * heads), (unsigned)(kItems / per_cta), 1);
+    cfg.gridDim = dim3((unsigned)units, (unsigned)(kItems / per_cta), 1);
     cfg.blockDim = dim3(kAttnJoinThreads, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -1756,6 +1789,7 @@ int w8a8_paged_attention(const uint16_t* q, int64_t ldq, const void* k_cache, co
     a.part_o = reinterpret_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(ws) + align_up(rows * D * 4, 256));
     a.grid = 0;
+    a.csize = 0;
     cudaStream_t st = (cudaStream_t)stream;
     if (k_scale)
         return D == 64 ? launch_attn_nq<64, true>(a, st) : D == 128 ? launch_attn_nq<128, true>(a, st)

@@ -207,6 +207,31 @@ def test_attention_long(D, Hkv, G, lens, int8):
         assert torch.equal(y, c.attend(q))       # the parts are joined in a fixed order
 
 
+@pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("D,G", [(64, 3), (128, 12), (256, 6)])
+def test_attention_shares_of_ragged_contexts(D, G, int8):
+    """Contexts long enough that CTAs take shares: units that begin and end inside a share, empty sequences between."""
+    c = Cache([0, 9000, 0, 0, 1, 6001, 128, 0, 4097, 0], 2, D, 8, int8, seed=G)
+    q = _q(10, 2 * G, D)
+    y = c.attend(q, y=torch.full_like(q, 3.0))
+    _check(c, q, y)
+    if D == 64:   # a page outside the cache in a long context: its tokens count as absent
+        table = c.table.clone()
+        table[1, 700] = -7
+        y = w8a8.paged_attention(q, c.k, c.v, table, c.lengths, k_scale=c.ks, v_scale=c.vs)
+        assert w8a8.get_device_error()[0] == w8a8.ERR_INVALID_ARG
+        d = Cache.__new__(Cache)
+        d.__dict__.update(c.__dict__)
+        keep = torch.ones(9000, dtype=torch.bool)
+        keep[700 * 8:701 * 8] = False
+        k, v = (c.rows(x, s, 1)[:, keep.cuda()] for x, s in ((c.k, c.ks), (c.v, c.vs)))
+        p = torch.softmax(torch.einsum("hgd,htd->hgt", q[1].double().view(2, G, D), k) * D ** -0.5, dim=2)
+        want = torch.einsum("hgt,htd->hgd", p, v).view(2 * G, D)
+        # the tolerance of _check, with its terms' values here: fp16 probabilities 2^-11, 9000 tokens 2^-23 each
+        av = torch.einsum("hgt,htd->hgd", p, v.abs()).view(2 * G, D)
+        assert ((y[1].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -9 * av).all()
+
+
 def test_attention_many_sequences():
     lens = [(i * 37) % 90 for i in range(600)]
     c = Cache(lens, 1, 64, 8, True)
