@@ -410,8 +410,11 @@ W8A8_API int w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, i
  * The context is split over the GPU and its parts are joined in a fixed order:
  * the same call gives the same bits again.  1 <= B <= 4096.  `ws` belongs to one
  * call at a time: calls that overlap on the GPU need workspaces of their own.
- * ws_bytes >= w8a8_paged_attention_workspace_size(B, Hq, Hkv, D). */
-W8A8_API size_t w8a8_paged_attention_workspace_size(int64_t B, int Hq, int Hkv, int D);
+ * ws_bytes >= w8a8_paged_attention_workspace_size(B, Hq, Hkv, D, int8,
+ * page_size, max_pages), int8 = 1 for a cache with scales; where that is 0
+ * (short contexts), ws may be NULL. */
+W8A8_API size_t w8a8_paged_attention_workspace_size(int64_t B, int Hq, int Hkv, int D, int int8, int page_size,
+                                                    int64_t max_pages);
 W8A8_API int w8a8_paged_attention(const uint16_t* q, int64_t ldq, const void* k_cache, const void* v_cache,
                                   const float* k_scale, const float* v_scale, const int32_t* block_table,
                                   int64_t ld_table, const int32_t* lengths, uint16_t* y, int64_t B, int Hq, int Hkv,

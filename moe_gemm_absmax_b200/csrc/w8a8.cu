@@ -1632,6 +1632,33 @@ constexpr int kAttnMaxMinB = 3;
 
 size_t attn_part_rows(int nq) { return (size_t)kAttnSms * kAttnMaxMinB * 2 * 8 * nq; }
 
+// How the CTAs divide the contexts: C > 0, clusters of C with a (sequence, head)
+// each; C = 0, shares of all chunks.  From the sizes alone, so that workspace
+// sizes are known.
+//
+// Clusters serve where that leaves a CTA few chunks; how few, goes by how much
+// of the GPU they fill (shares would fill all of it, but pay for the search and
+// the join).  8 heads of 128, int8, shares / clusters: 4 sequences of up to 1000
+// 9.6 / 8.5 us, of 4000 15.0 / 13.0; 16 of 2000 (8 chunks a CTA) 21.6 / 19.4, of
+// 4000 (16) 27.3 / 33.2; 64 of 1000 (8 chunks, one CTA a unit) 37.3 / 32.1, 256
+// of 2000 (16) 133 / 127.  Where a CTA fills an SM (D = 256, bf16), clusters of 8
+// do not pack (4 sequences of 500: 9.7 / 13.7 us, by fours 9.2), and many units a
+// CTA wait for one another's first loads (256 of 1000: 123 / 133).
+int attn_clusters(int64_t units, int64_t chunks, int minb) {
+    const int64_t slots = (int64_t)kAttnSms * minb;
+    int C = 8;
+    while (C > 1 && (C / 2 >= chunks || units * C > (minb == 1 && C == 8 ? slots * 3 / 4 : slots))) C /= 2;
+    const bool waits = minb == 1 && units > 2 * slots;
+    const int64_t few = waits ? 4 : (units * C >= slots ? 16 : (units * C * 2 >= slots ? 8 : 4));
+    return chunks <= few * C ? C : 0;
+}
+
+template <int D, bool INT8, int NQ>
+int attn_clusters_of(int64_t units, int64_t cap) {
+    using Cfg = AttnCfg<D, INT8, NQ>;
+    return attn_clusters(units, (cap + Cfg::CH - 1) / Cfg::CH, Cfg::kMinB);
+}
+
 template <int D, bool INT8, int NQ>
 int launch_attn(AttnArgs a, cudaStream_t st) {
     using Cfg = AttnCfg<D, INT8, NQ>;
@@ -1646,41 +1673,25 @@ int launch_attn(AttnArgs a, cudaStream_t st) {
             return W8A8_ERR_CUDA;
         attr_done[dev] = true;
     }
-    const int64_t heads = (int64_t)a.Hkv * a.qtiles;
-    const int64_t chunks = (a.cap + Cfg::CH - 1) / Cfg::CH;   // of a full sequence
-    // Clusters with a unit each, where that leaves a CTA few chunks; how few, goes
-    // by how much of the GPU they fill (shares would fill all of it, but pay for
-    // the search and the join).  8 heads of 128, int8, shares / clusters: 4
-    // sequences of up to 1000 9.6 / 8.5 us, of 4000 15.0 / 13.0; 16 of 2000 (8
-    // chunks a CTA) 21.6 / 19.4, of 4000 (16) 27.3 / 33.2; 64 of 1000 (8 chunks,
-    // one CTA a unit) 37.3 / 32.1, 256 of 2000 (16) 133 / 127.  Where a CTA fills an
-    // SM (D = 256, bf16), clusters of 8 do not pack (4 sequences of 500: 9.7 / 13.7
-    // us, by fours 9.2), and many units a CTA wait for one another's first loads
-    // (256 of 1000: 123 / 133).
-    const int64_t slots = (int64_t)kAttnSms * Cfg::kMinB;
-    const int64_t units = a.B * heads;
-    int C = 8;
-    while (C > 1 && (C / 2 >= chunks || units * C > (Cfg::kMinB == 1 && C == 8 ? slots * 3 / 4 : slots))) C /= 2;
-    const bool waits = Cfg::kMinB == 1 && units > 2 * slots;
-    const int64_t few = waits ? 4 : (units * C >= slots ? 16 : (units * C * 2 >= slots ? 8 : 4));
-    if (chunks <= few * C) {
-        a.csize = C;
-        a.grid = (int)(units * C);
-        cudaLaunchConfig_t cfg = {};
+    const int64_t units = (int64_t)a.B * a.Hkv * a.qtiles;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    a.csize = attn_clusters_of<D, INT8, NQ>(units, a.cap);
+    if (a.csize > 0) {
+        a.grid = (int)(units * a.csize);
         cfg.gridDim = dim3((unsigned)a.grid, 1, 1);
         cfg.blockDim = dim3(kAttnThreads, 1, 1);
         cfg.dynamicSmemBytes = Cfg::kBytes;
-        cfg.stream = st;
-        cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = (unsigned)C;
+        at[0].val.clusterDim.x = (unsigned)a.csize;
         at[0].val.clusterDim.y = 1;
         at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
         return cuda_status(cudaLaunchKernelEx(&cfg, kern, a));
     }
-    const int64_t most = units * chunks;                      // chunks, if every sequence were full
+    const int64_t most = units * ((a.cap + Cfg::CH - 1) / Cfg::CH);   // chunks, if every sequence were full
     a.grid = (int)(most < kAttnSms * Cfg::kMinB ? most : kAttnSms * Cfg::kMinB);
     kern<<<(unsigned)a.grid, kAttnThreads, Cfg::kBytes, st>>>(a);
     int rc = last_launch_status();
@@ -1690,11 +1701,8 @@ int launch_attn(AttnArgs a, cudaStream_t st) {
     constexpr int kItems = 8 * NQ * D / 4;
     int per_cta = kItems < kAttnJoinThreads ? kItems : kAttnJoinThreads;
     while (per_cta > 32 && units * (kItems / per_cta) < 4 * kAttnSms) per_cta /= 2;
-    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)units, (unsigned)(kItems / per_cta), 1);
     cfg.blockDim = dim3(kAttnJoinThreads, 1, 1);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
     pdl_config(cfg, at, true);
     return cuda_status(cudaLaunchKernelEx(&cfg, attn_join_kernel<D, Cfg::CH, NQ>, a, per_cta));
 }
@@ -1702,6 +1710,12 @@ int launch_attn(AttnArgs a, cudaStream_t st) {
 template <int D, bool INT8>
 int launch_attn_nq(const AttnArgs& a, cudaStream_t st) {
     return attn_nq(a.G) == 2 ? launch_attn<D, INT8, 2>(a, st) : launch_attn<D, INT8, 1>(a, st);
+}
+
+template <int D>
+int attn_clusters_d(int64_t units, int64_t cap, bool int8, int nq) {
+    return int8 ? (nq == 2 ? attn_clusters_of<D, true, 2>(units, cap) : attn_clusters_of<D, true, 1>(units, cap))
+                : (nq == 2 ? attn_clusters_of<D, false, 2>(units, cap) : attn_clusters_of<D, false, 1>(units, cap));
 }
 
 template <int D, bool INT8>
@@ -1742,9 +1756,18 @@ int w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ld
                                                                 : launch_append<256, false>(a, st);
 }
 
-size_t w8a8_paged_attention_workspace_size(int64_t B, int Hq, int Hkv, int D) {
-    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128 && D != 256)) return 0;
-    const size_t rows = attn_part_rows(attn_nq(Hq / Hkv));
+size_t w8a8_paged_attention_workspace_size(int64_t B, int Hq, int Hkv, int D, int int8, int page_size,
+                                           int64_t max_pages) {
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || page_size <= 0 || max_pages <= 0 ||
+        (D != 64 && D != 128 && D != 256))
+        return 0;
+    const int nq = attn_nq(Hq / Hkv);
+    const int64_t units = B * Hkv * ((Hq / Hkv + 8 * nq - 1) / (8 * nq)), cap = max_pages * page_size;
+    if ((D == 64 ? attn_clusters_d<64>(units, cap, int8 != 0, nq)
+         : D == 128 ? attn_clusters_d<128>(units, cap, int8 != 0, nq)
+                    : attn_clusters_d<256>(units, cap, int8 != 0, nq)) > 0)
+        return 0;
+    const size_t rows = attn_part_rows(nq);
     return align_up(rows * D * 4, 256) + align_up(rows * 8, 256);
 }
 
@@ -1752,7 +1775,7 @@ int w8a8_paged_attention(const uint16_t* q, int64_t ldq, const void* k_cache, co
                          const float* k_scale, const float* v_scale, const int32_t* block_table, int64_t ld_table,
                          const int32_t* lengths, uint16_t* y, int64_t B, int Hq, int Hkv, int D, int64_t num_pages,
                          int page_size, int64_t max_pages, float scale, void* ws, size_t ws_bytes, void* stream) {
-    if (!q || !k_cache || !v_cache || !block_table || !lengths || !y || !ws) return W8A8_ERR_INVALID_ARG;
+    if (!q || !k_cache || !v_cache || !block_table || !lengths || !y) return W8A8_ERR_INVALID_ARG;
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || num_pages <= 0 || max_pages <= 0 || ld_table < max_pages)
         return W8A8_ERR_INVALID_ARG;
     if ((k_scale == nullptr) != (v_scale == nullptr)) return W8A8_ERR_INVALID_ARG;
@@ -1763,7 +1786,9 @@ int w8a8_paged_attention(const uint16_t* q, int64_t ldq, const void* k_cache, co
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 16) ||
         !aligned(v_scale, 16) || !aligned(block_table, 4) || !aligned(lengths, 4) || !aligned(y, 16) || !aligned(ws, 256))
         return W8A8_ERR_INVALID_ARG;
-    if (ws_bytes < w8a8_paged_attention_workspace_size(B, Hq, Hkv, D)) return W8A8_ERR_WORKSPACE;
+    const size_t need = w8a8_paged_attention_workspace_size(B, Hq, Hkv, D, k_scale != nullptr, page_size, max_pages);
+    if (need > 0 && !ws) return W8A8_ERR_INVALID_ARG;
+    if (ws_bytes < need) return W8A8_ERR_WORKSPACE;
     AttnArgs a;
     a.q = q;
     a.ldq = ldq;

@@ -102,7 +102,7 @@ def lib() -> ctypes.CDLL:
                                         ctypes.POINTER(SharedExpertDebug), vp], i32),
         "w8a8_linear_epilogue": ([vp, i64, vp, vp, vp, i32, vp, i64, vp, i64, i64, i64, i64, vp, sz, vp], i32),
         "w8a8_kv_append": ([vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, i32, i32, i64, i32, vp], i32),
-        "w8a8_paged_attention_workspace_size": ([i64, i32, i32, i32], sz),
+        "w8a8_paged_attention_workspace_size": ([i64, i32, i32, i32, i32, i32, i64], sz),
         "w8a8_paged_attention": ([vp, i64, vp, vp, vp, vp, vp, i64, vp, vp, i64, i32, i32, i32, i64, i32, i64, f32, vp,
                                   sz, vp], i32),
         "w8a8_token_logprobs": ([vp, i32, i64, vp, i32, vp, vp, vp, vp, i64, i64, i32, vp], i32),
@@ -542,6 +542,10 @@ def _raw_stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+def _bytes(n: int, device) -> torch.Tensor:
+    return torch.empty_strided((n,), (1,), dtype=torch.uint8, device=device)
+
+
 def _on(t, dtype, name, shape, device):
     """Contiguous tensor of this type, shape and device; its address."""
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != device \
@@ -597,11 +601,11 @@ def linear_epilogue(x, qw, sw, bias=None, act: int = ACT_NONE, residual=None, y=
     if residual is not None:
         ldr, pr = _row_stride(residual, torch.bfloat16, "residual", dev, (M, N)), residual.data_ptr()
     if y is None:
-        y, ldy = x.new_empty((M, N)), N
+        y, ldy = torch.empty_strided((M, N), (N, 1), dtype=torch.bfloat16, device=dev), N
     else:
         ldy = _row_stride(y, torch.bfloat16, "y", dev, (M, N))
     if ws is None:
-        ws = x.new_empty(_linear_ws(M, N, K), dtype=torch.uint8)
+        ws = _bytes(_linear_ws(M, N, K), dev)
     _check(lib().w8a8_linear_epilogue(x.data_ptr(), ldx, pw, ps, pb, act, pr, ldr, y.data_ptr(), ldy, M, N, K,
                                       ws.data_ptr(), ws.numel(), raw_stream), "w8a8_linear_epilogue")
     return y
@@ -642,13 +646,12 @@ def kv_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, *, raw_
            "w8a8_kv_append")
 
 
-def paged_attention_workspace_size(B: int, Hq: int, Hkv: int, D: int) -> int:
-    return int(lib().w8a8_paged_attention_workspace_size(B, Hq, Hkv, D))
+def paged_attention_workspace_size(B: int, Hq: int, Hkv: int, D: int, int8: bool, page_size: int,
+                                   max_pages: int) -> int:
+    return int(lib().w8a8_paged_attention_workspace_size(B, Hq, Hkv, D, int8, page_size, max_pages))
 
 
-@functools.lru_cache(maxsize=1024)
-def _attention_ws(B: int, Hq: int, Hkv: int, D: int) -> int:
-    return max(paged_attention_workspace_size(B, Hq, Hkv, D), 256)
+_attention_ws = functools.lru_cache(maxsize=4096)(paged_attention_workspace_size)
 
 
 @_placed
@@ -669,16 +672,21 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, scale: float | No
     if block_table.shape[0] != B:
         raise ValueError("block_table must have a row per sequence")
     if y is None:
-        y = q.new_empty((B, Hq, D))
+        y = torch.empty_strided((B, Hq, D), (Hq * D, D, 1), dtype=torch.bfloat16, device=dev)
         py = y.data_ptr()
     else:
         py = _on(y, torch.bfloat16, "y", (B, Hq, D), dev)
+    max_pages, pws, nws = block_table.shape[1], None, 0
     if ws is None:
-        ws = q.new_empty(_attention_ws(B, Hq, Hkv, D), dtype=torch.uint8)
+        nws = _attention_ws(B, Hq, Hkv, D, pks is not None, page, max_pages)
+        if nws:
+            ws = _bytes(nws, dev)
+    if ws is not None:
+        pws, nws = ws.data_ptr(), ws.numel()
     _check(lib().w8a8_paged_attention(q.data_ptr(), ldq, pkc, pvc, pks, pvs, block_table.data_ptr(), ld_table,
                                       _on(lengths, torch.int32, "lengths", (B,), dev), py, B, Hq, Hkv, D, pages, page,
-                                      block_table.shape[1], D ** -0.5 if scale is None else scale, ws.data_ptr(),
-                                      ws.numel(), raw_stream), "w8a8_paged_attention")
+                                      max_pages, D ** -0.5 if scale is None else scale, pws, nws, raw_stream),
+           "w8a8_paged_attention")
     return y
 
 
@@ -704,13 +712,14 @@ def token_logprobs(logits, tokens=None, topk: int = 0, entropy: bool = True, *, 
             raise ValueError("tokens must be [M] or [M, G]")
         pt = _on(tokens, torch.int32, "tokens", tokens.shape, dev)
         G = 1 if tokens.dim() == 1 else tokens.shape[1]
-        logprob = logits.new_empty(tokens.shape, dtype=f32)
+        logprob = torch.empty_like(tokens, dtype=f32)
         pl = logprob.data_ptr()
     if entropy:
-        h = logits.new_empty(M, dtype=f32)
+        h = torch.empty_strided((M,), (1,), dtype=f32, device=dev)
         ph = h.data_ptr()
     if topk > 0:
-        ids, top = logits.new_empty((M, topk), dtype=torch.int32), logits.new_empty((M, topk), dtype=f32)
+        ids = torch.empty_strided((M, topk), (topk, 1), dtype=torch.int32, device=dev)
+        top = torch.empty_strided((M, topk), (topk, 1), dtype=f32, device=dev)
         pi, pv = ids.data_ptr(), top.data_ptr()
     _check(lib().w8a8_token_logprobs(logits.data_ptr(), int(dtype is f32), ld, pt, G, pl, ph, pi, pv, M, V, topk,
                                      raw_stream), "w8a8_token_logprobs")

@@ -56,19 +56,21 @@ ATTEND = dict(q=P, ldq=256, kc=P, vc=P, ks=P, vs=P, table=P, ld_table=8, lengths
 
 @pytest.mark.parametrize("change,status", [
     (dict(q=None), INVALID), (dict(kc=None), INVALID), (dict(table=None), INVALID), (dict(lengths=None), INVALID),
-    (dict(y=None), INVALID), (dict(ws=None), INVALID), (dict(ks=None), INVALID), (dict(B=0), INVALID),
+    (dict(y=None), INVALID), (dict(max_pages=4000, ld_table=4000, ws=None), INVALID), (dict(ks=None), INVALID), (dict(B=0), INVALID),
     (dict(Hq=5), INVALID), (dict(Hkv=0), INVALID), (dict(max_pages=0), INVALID), (dict(ld_table=7), INVALID),
     (dict(ldq=248), INVALID), (dict(ldq=260), INVALID), (dict(q=ODD), INVALID), (dict(vs=ODD), INVALID),
     (dict(ws=ctypes.c_void_p(0x10010)), INVALID), (dict(D=80), UNSUPPORTED), (dict(page=24), UNSUPPORTED),
-    (dict(B=4097), UNSUPPORTED), (dict(ws_bytes=1024), WORKSPACE)])
+    (dict(B=4097), UNSUPPORTED), (dict(max_pages=4000, ld_table=4000, ws_bytes=1024), WORKSPACE)])
 def test_attention_refuses(L, change, status):
     assert L.w8a8_paged_attention(*_with(ATTEND, **change)) == status
 
 
 def test_attention_workspace(L):
     size = L.w8a8_paged_attention_workspace_size
-    assert size(1, 8, 8, 128) == size(4096, 8, 8, 128) > 0       # the work split's grid is fixed
-    assert size(1, 7, 2, 128) == size(0, 8, 8, 128) == size(1, 8, 8, 96) == 0
+    # the work split's grid is fixed, and so is what its parts take; short contexts need none
+    assert size(1, 8, 8, 128, 1, 16, 4000) == size(64, 8, 8, 128, 0, 64, 1000) > 0
+    assert size(1, 8, 8, 128, 1, 16, 60) == 0
+    assert size(1, 7, 2, 128, 1, 16, 4000) == size(0, 8, 8, 128, 1, 16, 4000) == size(1, 8, 8, 96, 1, 16, 4000) == 0
 
 
 LOGPROBS = dict(logits=P, f32=0, ld=100, tokens=P, G=1, logprob=P, entropy=P, ids=P, top=P, M=2, V=100, topk=5, stream=None)
