@@ -52,14 +52,19 @@ struct Tc2Smem {
     static constexpr int kB1 = (BN / 2) * kTcBK;             // one k block of B: 16 / 10 / 9 KB (multiples of 1 KB)
     static constexpr int kA = kKB * kA1;
     static constexpr int kB = kKB * kB1;
-    static constexpr int kStages = BN == 256 ? 6 : (BN == 144 ? 4 : (FUSED ? 7 : 8));
+    static constexpr int kStages = BN == 256 ? (FUSED ? 5 : 6) : (BN == 144 ? 4 : (FUSED ? 6 : 8));
     static constexpr int kTiles = kStages * (kA + kB);
-    static constexpr int kBars = (2 * kStages + 2 + 2 + 1) * 8;
-    // each epilogue warp's copy of the tile's column scales (fp32)
-    static constexpr int kEpiOff = kTiles + (kBars + 16 + 15) / 16 * 16;
-    // (FUSED: each warp's 32 rows x 32 columns of bf16 on their way in or out,
-    // and the chunk's 32 column scales and biases)
-    static constexpr int kEpiWarp = FUSED ? 32 * 64 + 2 * 32 * 4 : BN * 4;
+    // FUSED: three chunks of 32 rows x kCW columns of bf16 per epilogue warp, on
+    // their way in or out
+    static constexpr int kCW = BN % 32 ? 16 : 32;
+    static constexpr int kChunk = 32 * kCW * 2;
+    static constexpr int kRing = FUSED ? kTc2Epi * 3 * kChunk : 0;
+    static constexpr int kBarOff = kTiles + kRing;
+    static constexpr int kBars = (2 * kStages + 2 + 2 + 1 + (FUSED ? 3 * kTc2Epi : 0)) * 8;
+    // each epilogue warp's copy of the tile's column scales (fp32); FUSED: of a
+    // chunk's column scales and biases
+    static constexpr int kEpiOff = kBarOff + (kBars + 16 + 15) / 16 * 16;
+    static constexpr int kEpiWarp = FUSED ? 2 * kCW * 4 : BN * 4;
     static constexpr int kEpiBytes = kTc2Epi * kEpiWarp;
     static constexpr int kBytes = 1024 + kEpiOff + kEpiBytes;
     static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
@@ -106,9 +111,147 @@ __device__ __forceinline__ void tc2_commit_pair(uint64_t* bar) {
         : "memory");
 }
 
-template <int EPI, int BN = 256>
-__global__ void __launch_bounds__(kTc2Threads, 1)
-    gemm_i8_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, TcParams p) {
+// TMA tile store from this CTA's shared memory, in the thread's current bulk group.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t smem_src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_src), "r"(x), "r"(y)
+                 : "memory");
+}
+
+// Epilogue of the linear with bias, activation and residual, one warp.  Residual
+// and output cross global memory as TMA boxes of 32 rows x kCW columns through
+// a ring of three chunks of shared memory: the residual of the chunk after next
+// is on its way while one is computed in place and the last one leaves.  (As
+// loads and stores of the warp -- even 64 bytes a row, eight rows an instruction
+// -- they took three quarters of the load-store unit's wavefronts at K = 512 and
+// set the pace there.)  The boxes' swizzle is what keeps the accumulator's layout
+// (lane = row) free of bank conflicts: 16-byte unit u of row r lies at u ^ (r / 2 % 4)
+// for 64-byte rows, u ^ (r / 4 % 2) for 32-byte ones.
+template <int BN>
+__device__ __forceinline__ void tc2_fused_epilogue(const CUtensorMap* tmY, const CUtensorMap* tmR, const TcParams& p,
+                                                   uint8_t* smem, uint64_t* rbar, float* epi_scratch, uint64_t* tfull,
+                                                   uint64_t* tempty, volatile int* abort_flag, uint32_t tmem_base,
+                                                   int rank, int cluster_id, int nclusters, int num_tiles) {
+    using SM = Tc2Smem<BN, true>;
+    constexpr int CW = SM::kCW, kChunks = (BN + 2 * CW - 1) / (2 * CW), UN = CW / 8;   // 16-byte units of a row
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quarter = warp & 3, half = (warp - 2) >> 2;   // chunks c = CW half + 2 CW i
+    const uint32_t tempty_leader0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    uint8_t* ring = smem + SM::kTiles + (warp - 2) * 3 * SM::kChunk;
+    float* sb = epi_scratch + (warp - 2) * (SM::kEpiWarp / 4);   // CW scales, CW biases
+    const bool has_res = p.f.res != nullptr;
+    const int swz = UN == 4 ? (lane >> 1) & 3 : (lane >> 2) & 1;
+    auto first_row = [&](int tile) { return tile % p.num_m_tiles * kTc2BM + rank * 128 + quarter * 32; };
+    auto first_col = [&](int tile) { return tile / p.num_m_tiles * BN; };
+    // chunk c of a tile lies in the output at all; if not, neither do the warp's later ones of this tile
+    auto inside = [&](int tile, int c) { return c < BN && first_col(tile) + c < p.N && first_row(tile) < p.M; };
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // residual loads run ahead of the chunks by two
+    int ltile = cluster_id, lc = CW * half, issued = 0, done = 0;
+    auto load_next = [&]() {   // one lane
+        while (ltile < num_tiles && !inside(ltile, lc)) {
+            ltile += nclusters;
+            lc = CW * half;
+        }
+        if (ltile >= num_tiles) return;
+        const int b = issued % 3;
+        mbar_arrive_expect_tx(&rbar[b], SM::kChunk);
+        tma_load_2d(ring + b * SM::kChunk, tmR, &rbar[b], first_col(ltile) + lc, first_row(ltile));
+        ++issued;
+        lc += 2 * CW;
+    };
+    if (lane == 0) {
+        prefetch_tensormap(tmY);
+        if (has_res) {
+            prefetch_tensormap(tmR);
+            load_next();
+            load_next();
+        }
+    }
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int tile = cluster_id; ok && tile < num_tiles; tile += nclusters) {
+        const int row0 = first_row(tile), col0 = first_col(tile), row = row0 + lane;
+        const float sxr = row < p.M ? __ldcg(p.sx + row) : 0.0f;   // written by the kernel that was waited for
+        float swc[kChunks], bic[kChunks];
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int n = col0 + CW * half + 2 * CW * i + (lane & (CW - 1));
+            swc[i] = n < p.N ? __ldg(p.sw + n) : 0.0f;
+            bic[i] = p.f.bias && n < p.N ? __ldg(p.f.bias + n) : 0.0f;
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, (kKernelIdGemmTc2 << 16) | 6)))
+            break;
+        tc_fence_after();
+        const uint32_t tq = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN + CW * half);
+        uint32_t r[2][CW];
+        auto tmem_load = [&](uint32_t (&v)[CW], uint32_t at) {
+            if constexpr (CW == 32) tmem_ld_32x32b_x32(at, v);
+            else tmem_ld_32x32b_x16(at, v);
+        };
+        tmem_load(r[0], tq);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = CW * half + 2 * CW * i;
+            if (c >= BN || col0 + c >= p.N || row0 >= p.M) break;   // as inside()
+            const int b = done % 3;
+            // the chunk's place is free (its last store has been read: awaited below) or holds the residual
+            if (has_res) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&rbar[b], (uint32_t)(done / 3) & 1u, abort_flag,
+                                                               (kKernelIdGemmTc2 << 16) | 7));
+                if (!ok) break;
+            }
+            __syncwarp();
+            if (lane < CW) {
+                sb[lane] = swc[i];
+                sb[CW + lane] = bic[i];
+            }
+            __syncwarp();
+            tc_wait_ld();
+            if (i + 1 < kChunks && c + 2 * CW < BN) tmem_load(r[(i + 1) & 1], tq + (uint32_t)(2 * CW * (i + 1)));
+            uint4* own = reinterpret_cast<uint4*>(ring + b * SM::kChunk) + lane * UN;
+#pragma unroll
+            for (int v = 0; v < UN; ++v) {
+                uint4 res = make_uint4(0, 0, 0, 0);
+                if (has_res) res = own[v ^ swz];
+                own[v ^ swz] = epi_fused8(r[i & 1] + 8 * v, sxr, sb + 8 * v, sb + CW + 8 * v, res, p.f.act);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the copy engine reads them
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(tmY, smem_u32(ring + b * SM::kChunk), col0 + c, row0);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // the chunk before this one has left
+                if (has_res) load_next();
+            }
+            ++done;
+        }
+        tc_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty_leader0 + (uint32_t)(acc * 8));
+        if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1u;
+        }
+    }
+    if (lane == 0) {
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        // after a wait that ran out: residuals still on their way land before the CTA exits
+        for (; done < issued; ++done)
+            mbar_wait_bounded(&rbar[done % 3], (uint32_t)(done / 3) & 1u, nullptr, (kKernelIdGemmTc2 << 16) | 8, 100000000ull);
+    }
+    __syncwarp();
+}
+
+// tmY, tmR (kEpiFused): output and residual as boxes of 32 rows x kCW columns,
+// swizzled over their row width.
+template <int EPI, int BN>
+__device__ __forceinline__ void tc2_run(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap* tmY,
+                                        const CUtensorMap* tmR, const TcParams& p) {
     static_assert(EPI == kEpiBf16 || EPI == kEpiS32 || EPI == kEpiMoeGated || EPI == kEpiFused, "dense epilogues");
     static_assert(BN % 16 == 0 && (BN / 2) % 8 == 0 && BN <= 256, "pair tile width");
     constexpr int kCols = 2 * BN <= 256 ? 256 : 512;   // two accumulators of BN columns (a power of two)
@@ -117,13 +260,14 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = smem + SM::kStages * SM::kA;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kTiles);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kBarOff);
     uint64_t* full = bars;                      // leader only
     uint64_t* empty = bars + SM::kStages;        // both
     uint64_t* tfull = empty + SM::kStages;       // both
     uint64_t* tempty = tfull + 2;               // leader only
     uint64_t* mma_done = tempty + 2;            // leader only
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+    uint64_t* rbars = mma_done + 1;             // kEpiFused: three per epilogue warp, its chunks' residuals
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbars + (EPI == kEpiFused ? 3 * kTc2Epi : 0));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     float* epi_scratch = reinterpret_cast<float*>(smem + SM::kEpiOff);
 
@@ -141,6 +285,8 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
             mbar_init(&tempty[b], 2 * kTc2Epi);   // one arrival per epilogue warp of the pair
         }
         mbar_init(mma_done, 1);
+        if (EPI == kEpiFused)
+            for (int i = 0; i < 3 * kTc2Epi; ++i) mbar_init(&rbars[i], 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -252,9 +398,12 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
         }
     } else {
         // ------------------------------------------------------------ epilogue (both CTAs)
+        if constexpr (EPI == kEpiFused) {
+            tc2_fused_epilogue<BN>(tmY, tmR, p, smem, rbars + (warp - 2) * 3, epi_scratch, tfull, tempty, abort_flag,
+                                   tmem_base, (int)rank, cluster_id, nclusters, num_tiles);
+        } else {
         const int quarter = warp & 3;              // TMEM lanes [32 q, 32 q + 32)
         const int chalf = (warp - 2) >> 2;         // chunks c = 32 chalf + 64 i
-        if (EPI == kEpiFused) asm volatile("griddepcontrol.wait;" ::: "memory");
         const uint32_t tempty_leader0 = mapa_shared(smem_u32(&tempty[0]), 0);
         float* sw_s = epi_scratch + (warp - 2) * (SM::kEpiWarp / 4);   // this warp's copy of the tile's column scales
         int acc = 0;
@@ -265,7 +414,6 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
             const bool row_ok = row < p.M;
             float sxr = 0.0f;
             if ((EPI == kEpiBf16 || EPI == kEpiMoeGated) && row_ok) sxr = __ldg(p.sx + row);
-            if (EPI == kEpiFused && row_ok) sxr = __ldcg(p.sx + row);   // written by the kernel that it waited for
             if (EPI == kEpiBf16 || EPI == kEpiMoeGated) {
                 // the tile's BN column scales (N % 8 == 0: a 4-column vector is all in or all out)
                 __syncwarp();   // the previous tile's reads are done
@@ -276,32 +424,6 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
                     *reinterpret_cast<float4*>(sw_s + 4 * v) = sv;
                 }
                 __syncwarp();
-            }
-            // kEpiFused: global memory is read and written 64 bytes a row, eight rows
-            // an instruction (lane = 4 row + 16-byte unit); the warp's 32 x 32 chunk
-            // changes hands with the accumulator's layout (lane = row) through 2 KB
-            // of shared memory whose units are XORed with the row pair, so that
-            // neither side has bank conflicts.  The tile's residual is all in
-            // flight before the accumulator is waited for.
-            constexpr int kChunks = (BN + 63) / 64;
-            const int frow = mt * kTc2BM + (int)rank * 128 + quarter * 32 + (lane >> 2);   // + 8 v
-            const int fcol = nt * BN + 32 * chalf + 8 * (lane & 3);                        // + 64 i
-            uint4 res[EPI == kEpiFused ? kChunks : 1][4];
-            float swc[EPI == kEpiFused ? kChunks : 1], bic[EPI == kEpiFused ? kChunks : 1];
-            if constexpr (EPI == kEpiFused) {
-#pragma unroll
-                for (int i = 0; i < kChunks; ++i) {
-                    const bool col_ok = 32 * chalf + 64 * i + 8 * (lane & 3) < BN && fcol + 64 * i < p.N;
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        res[i][v] = make_uint4(0, 0, 0, 0);
-                        if (p.f.res && col_ok && frow + 8 * v < p.M)
-                            res[i][v] = ld_residual16(p.f.res + (int64_t)(frow + 8 * v) * p.f.ldr + fcol + 64 * i);
-                    }
-                    const int n = nt * BN + 32 * chalf + 64 * i + lane;
-                    swc[i] = n < p.N ? __ldg(p.sw + n) : 0.0f;
-                    bic[i] = p.f.bias && n < p.N ? __ldg(p.f.bias + n) : 0.0f;
-                }
             }
             if (!mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, (kKernelIdGemmTc2 << 16) | 6)) break;
             tc_fence_after();
@@ -361,52 +483,18 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
                 }
             };
             uint32_t ra[32], rb[32];
-            if constexpr (EPI == kEpiFused) {
-                uint4* ex = reinterpret_cast<uint4*>(sw_s);          // [32 rows][4 units]
-                float* sb = sw_s + 32 * 64 / 4;                      // 32 scales, 32 biases
-                const int mine = lane * 4, mx = (lane >> 1) & 3;     // row `lane`
-                const int gx = lane ^ ((lane >> 3) & 3);             // row lane / 4 + 8 v, unit lane % 4: 32 v + gx
-                tmem_ld_32x32b_x32(tq + (uint32_t)(32 * chalf), ra);
-#pragma unroll
-                for (int i = 0; i < kChunks; ++i) {
-                    const int c = 32 * chalf + 64 * i;
-                    if (c >= BN) break;
-                    __syncwarp();   // the previous chunk has left
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) ex[32 * v + gx] = res[i][v];
-                    sb[lane] = swc[i];
-                    sb[32 + lane] = bic[i];
-                    __syncwarp();
-                    tc_wait_ld();
-                    if (c + 64 < BN) tmem_ld_32x32b_x32(tq + (uint32_t)(c + 64), (i & 1) ? ra : rb);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        ex[mine + (v ^ mx)] = epi_fused8(((i & 1) ? rb : ra) + 8 * v, sxr, sb + 8 * v, sb + 32 + 8 * v,
-                                                         ex[mine + (v ^ mx)], p.f.act);
-                    __syncwarp();
-                    if (c + 8 * (lane & 3) < BN && fcol + 64 * i < p.N) {
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            if (frow + 8 * v < p.M)
-                                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) +
-                                                          (int64_t)(frow + 8 * v) * p.f.ldy + fcol + 64 * i) =
-                                    ex[32 * v + gx];
-                    }
-                }
-            } else {
-                int c = 32 * chalf;
-                if (c < BN) tmem_ld_32x32b_x32(tq + (uint32_t)c, ra);
-                while (c < BN) {
-                    tc_wait_ld();
-                    if (c + 64 < BN) tmem_ld_32x32b_x32(tq + (uint32_t)(c + 64), rb);
-                    chunk(ra, c);
-                    c += 64;
-                    if (c >= BN) break;
-                    tc_wait_ld();
-                    if (c + 64 < BN) tmem_ld_32x32b_x32(tq + (uint32_t)(c + 64), ra);
-                    chunk(rb, c);
-                    c += 64;
-                }
+            int c = 32 * chalf;
+            if (c < BN) tmem_ld_32x32b_x32(tq + (uint32_t)c, ra);
+            while (c < BN) {
+                tc_wait_ld();
+                if (c + 64 < BN) tmem_ld_32x32b_x32(tq + (uint32_t)(c + 64), rb);
+                chunk(ra, c);
+                c += 64;
+                if (c >= BN) break;
+                tc_wait_ld();
+                if (c + 64 < BN) tmem_ld_32x32b_x32(tq + (uint32_t)(c + 64), ra);
+                chunk(rb, c);
+                c += 64;
             }
             tc_fence_before();
             __syncwarp();
@@ -415,6 +503,7 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
                 acc = 0;
                 acc_phase ^= 1u;
             }
+        }
         }
     }
 
@@ -425,6 +514,20 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kCols) : "memory");
     }
+}
+
+template <int EPI, int BN = 256>
+__global__ void __launch_bounds__(kTc2Threads, 1)
+    gemm_i8_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, TcParams p) {
+    static_assert(EPI != kEpiFused, "gemm_i8_tc2_fused_kernel");
+    tc2_run<EPI, BN>(tmA, tmB, nullptr, nullptr, p);
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kTc2Threads, 1)
+    gemm_i8_tc2_fused_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                             const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmR, TcParams p) {
+    tc2_run<kEpiFused, BN>(tmA, tmB, &tmY, &tmR, p);
 }
 
 }  // namespace w8a8

@@ -88,6 +88,19 @@ bool make_tmap_i8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 matrix [rows, cols] (row stride ld elements) as boxes of 32 rows x box_cols (32 or 16), swizzled over their width.
+bool make_tmap_bf16_out(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_cols) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t gdim[2] = {cols, rows};
+    cuuint64_t gstride[1] = {ld * 2};
+    cuuint32_t box[2] = {box_cols, 32};
+    cuuint32_t estride[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), gdim, gstride, box, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ----------------------------------------------------------------- tcgen05 GEMM
 template <int BN, int STAGES, int EPI, int NACC, int NEPI = 4>
 int launch_tc(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st) {
@@ -118,7 +131,10 @@ int launch_tc(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st) {
 template <int EPI, int BN>
 int launch_tc2_bn(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st) {
     using SM = Tc2Smem<BN, EPI == kEpiFused>;
-    auto kern = gemm_i8_tc2_kernel<EPI, BN>;
+    const auto kern = [] {
+        if constexpr (EPI == kEpiFused) return gemm_i8_tc2_fused_kernel<BN>;
+        else return gemm_i8_tc2_kernel<EPI, BN>;
+    }();
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return W8A8_ERR_CUDA;
     if (dev < 0 || dev >= kMaxDevices) return W8A8_ERR_UNSUPPORTED;
@@ -151,12 +167,20 @@ int launch_tc2_bn(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st)
     const int tiles = p.num_m_tiles * p.num_n_tiles;
     const int clusters = tiles < max_clusters[dev] ? tiles : max_clusters[dev];
     cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
-    if (EPI == kEpiFused) {   // set up while the activation quant before it finishes
+    if constexpr (EPI == kEpiFused) {
+        CUtensorMap ty, tr;
+        if (!make_tmap_bf16_out(&ty, p.out, (uint64_t)p.M, (uint64_t)p.N, (uint64_t)p.f.ldy, SM::kCW)) return W8A8_ERR_CUDA;
+        tr = ty;
+        if (p.f.res && !make_tmap_bf16_out(&tr, p.f.res, (uint64_t)p.M, (uint64_t)p.N, (uint64_t)p.f.ldr, SM::kCW))
+            return W8A8_ERR_CUDA;
+        // set up while the activation quant before it finishes
         at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.numAttrs = 2;
+        return cuda_status(cudaLaunchKernelEx(&cfg, kern, ta, tb, ty, tr, p));
+    } else {
+        return cuda_status(cudaLaunchKernelEx(&cfg, kern, ta, tb, p));
     }
-    return cuda_status(cudaLaunchKernelEx(&cfg, kern, ta, tb, p));
 }
 
 // Pair-tile width: 256 columns, or 160 / 144 where a narrower tile's better
