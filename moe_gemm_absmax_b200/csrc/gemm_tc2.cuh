@@ -43,8 +43,13 @@ constexpr int kKernelIdGemmTc2 = 4;
 // per-stage hand-off (MMA completion -> empty -> producer -> full -> MMA
 // thread): one k block for the 256 and 160 tiles (512 / 320 cycles of MMA),
 // two for the 144 tile (2 x 288).
-template <int BN, bool FUSED = false>
+// NEF: epilogue warps of the linear with bias, activation and residual (0: the
+// other epilogues).
+template <int BN, int NEF = 0>
 struct Tc2Smem {
+    static constexpr bool FUSED = NEF > 0;
+    static constexpr int kEpi = FUSED ? NEF : kTc2Epi;
+    static constexpr int kThreads = 64 + 32 * kEpi;
     // k blocks per stage: the 144 tile (a few hundred tokens, one tile per
     // cluster) takes two, halving the stage hand-offs per MMA
     static constexpr int kKB = BN == 144 ? 2 : 1;
@@ -56,16 +61,16 @@ struct Tc2Smem {
     static constexpr int kTiles = kStages * (kA + kB);
     // FUSED: three chunks of 32 rows x kCW columns of bf16 per epilogue warp, on
     // their way in or out
-    static constexpr int kCW = BN % 32 ? 16 : 32;
+    static constexpr int kCW = NEF == 8 && BN % 32 == 0 ? 32 : 16;
     static constexpr int kChunk = 32 * kCW * 2;
-    static constexpr int kRing = FUSED ? kTc2Epi * 3 * kChunk : 0;
+    static constexpr int kRing = FUSED ? kEpi * 3 * kChunk : 0;
     static constexpr int kBarOff = kTiles + kRing;
-    static constexpr int kBars = (2 * kStages + 2 + 2 + 1 + (FUSED ? 3 * kTc2Epi : 0)) * 8;
+    static constexpr int kBars = (2 * kStages + 2 + 2 + 1 + (FUSED ? 3 * kEpi : 0)) * 8;
     // each epilogue warp's copy of the tile's column scales (fp32); FUSED: of a
     // chunk's column scales and biases
     static constexpr int kEpiOff = kBarOff + (kBars + 16 + 15) / 16 * 16;
     static constexpr int kEpiWarp = FUSED ? 2 * kCW * 4 : BN * 4;
-    static constexpr int kEpiBytes = kTc2Epi * kEpiWarp;
+    static constexpr int kEpiBytes = kEpi * kEpiWarp;
     static constexpr int kBytes = 1024 + kEpiOff + kEpiBytes;
     static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
@@ -126,17 +131,23 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sm
 // loads and stores of the warp -- even 64 bytes a row, eight rows an instruction
 // -- they took three quarters of the load-store unit's wavefronts at K = 512 and
 // set the pace there.)  The boxes' swizzle is what keeps the accumulator's layout
-// (lane = row) free of bank conflicts: 16-byte unit u of row r lies at u ^ (r / 2 % 4)
+// (lane = row) free of bank conflicts.  16 warps with 16-column chunks where the
+// epilogue shows: few k blocks a tile (M = 4096, K = 512, N = 17408, SiLU, residual:
+// 113 us against 132 with 8 warps and 32-column chunks) or one wave of tiles (M =
+// 1000, K = N = 5120: 34.5 against 37.3); 8 where the MMAs of many tiles hide it and
+// half the boxes are the cheaper (K = 5120: 254 us against 259).  The swizzle:
+// 16-byte unit u of row r lies at u ^ (r / 2 % 4)
 // for 64-byte rows, u ^ (r / 4 % 2) for 32-byte ones.
-template <int BN>
+template <int BN, int NEF>
 __device__ __forceinline__ void tc2_fused_epilogue(const CUtensorMap* tmY, const CUtensorMap* tmR, const TcParams& p,
                                                    uint8_t* smem, uint64_t* rbar, float* epi_scratch, uint64_t* tfull,
                                                    uint64_t* tempty, volatile int* abort_flag, uint32_t tmem_base,
                                                    int rank, int cluster_id, int nclusters, int num_tiles) {
-    using SM = Tc2Smem<BN, true>;
-    constexpr int CW = SM::kCW, kChunks = (BN + 2 * CW - 1) / (2 * CW), UN = CW / 8;   // 16-byte units of a row
+    using SM = Tc2Smem<BN, NEF>;
+    constexpr int CW = SM::kCW, NG = NEF / 4, kChunks = (BN + NG * CW - 1) / (NG * CW);
+    constexpr int UN = CW / 8;                               // 16-byte units of a row
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int quarter = warp & 3, half = (warp - 2) >> 2;   // chunks c = CW half + 2 CW i
+    const int quarter = warp & 3, half = (warp - 2) >> 2;   // chunks c = CW half + NG CW i
     const uint32_t tempty_leader0 = mapa_shared(smem_u32(&tempty[0]), 0);
     uint8_t* ring = smem + SM::kTiles + (warp - 2) * 3 * SM::kChunk;
     float* sb = epi_scratch + (warp - 2) * (SM::kEpiWarp / 4);   // CW scales, CW biases
@@ -160,7 +171,7 @@ __device__ __forceinline__ void tc2_fused_epilogue(const CUtensorMap* tmY, const
         mbar_arrive_expect_tx(&rbar[b], SM::kChunk);
         tma_load_2d(ring + b * SM::kChunk, tmR, &rbar[b], first_col(ltile) + lc, first_row(ltile));
         ++issued;
-        lc += 2 * CW;
+        lc += NG * CW;
     };
     if (lane == 0) {
         prefetch_tensormap(tmY);
@@ -179,7 +190,7 @@ __device__ __forceinline__ void tc2_fused_epilogue(const CUtensorMap* tmY, const
         float swc[kChunks], bic[kChunks];
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-            const int n = col0 + CW * half + 2 * CW * i + (lane & (CW - 1));
+            const int n = col0 + CW * half + NG * CW * i + (lane & (CW - 1));
             swc[i] = n < p.N ? __ldg(p.sw + n) : 0.0f;
             bic[i] = p.f.bias && n < p.N ? __ldg(p.f.bias + n) : 0.0f;
         }
@@ -195,7 +206,7 @@ __device__ __forceinline__ void tc2_fused_epilogue(const CUtensorMap* tmY, const
         tmem_load(r[0], tq);
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-            const int c = CW * half + 2 * CW * i;
+            const int c = CW * half + NG * CW * i;
             if (c >= BN || col0 + c >= p.N || row0 >= p.M) break;   // as inside()
             const int b = done % 3;
             // the chunk's place is free (its last store has been read: awaited below) or holds the residual
@@ -211,7 +222,7 @@ __device__ __forceinline__ void tc2_fused_epilogue(const CUtensorMap* tmY, const
             }
             __syncwarp();
             tc_wait_ld();
-            if (i + 1 < kChunks && c + 2 * CW < BN) tmem_load(r[(i + 1) & 1], tq + (uint32_t)(2 * CW * (i + 1)));
+            if (i + 1 < kChunks && c + NG * CW < BN) tmem_load(r[(i + 1) & 1], tq + (uint32_t)(NG * CW * (i + 1)));
             uint4* own = reinterpret_cast<uint4*>(ring + b * SM::kChunk) + lane * UN;
 #pragma unroll
             for (int v = 0; v < UN; ++v) {
@@ -249,13 +260,13 @@ __device__ __forceinline__ void tc2_fused_epilogue(const CUtensorMap* tmY, const
 
 // tmY, tmR (kEpiFused): output and residual as boxes of 32 rows x kCW columns,
 // swizzled over their row width.
-template <int EPI, int BN>
+template <int EPI, int BN, int NEF = 0>
 __device__ __forceinline__ void tc2_run(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap* tmY,
                                         const CUtensorMap* tmR, const TcParams& p) {
     static_assert(EPI == kEpiBf16 || EPI == kEpiS32 || EPI == kEpiMoeGated || EPI == kEpiFused, "dense epilogues");
     static_assert(BN % 16 == 0 && (BN / 2) % 8 == 0 && BN <= 256, "pair tile width");
     constexpr int kCols = 2 * BN <= 256 ? 256 : 512;   // two accumulators of BN columns (a power of two)
-    using SM = Tc2Smem<BN, EPI == kEpiFused>;
+    using SM = Tc2Smem<BN, NEF>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
@@ -267,7 +278,7 @@ __device__ __forceinline__ void tc2_run(const CUtensorMap& tmA, const CUtensorMa
     uint64_t* tempty = tfull + 2;               // leader only
     uint64_t* mma_done = tempty + 2;            // leader only
     uint64_t* rbars = mma_done + 1;             // kEpiFused: three per epilogue warp, its chunks' residuals
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbars + (EPI == kEpiFused ? 3 * kTc2Epi : 0));
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbars + (EPI == kEpiFused ? 3 * SM::kEpi : 0));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     float* epi_scratch = reinterpret_cast<float*>(smem + SM::kEpiOff);
 
@@ -282,11 +293,11 @@ __device__ __forceinline__ void tc2_run(const CUtensorMap& tmA, const CUtensorMa
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 2 * kTc2Epi);   // one arrival per epilogue warp of the pair
+            mbar_init(&tempty[b], 2 * SM::kEpi);   // one arrival per epilogue warp of the pair
         }
         mbar_init(mma_done, 1);
         if (EPI == kEpiFused)
-            for (int i = 0; i < 3 * kTc2Epi; ++i) mbar_init(&rbars[i], 1);
+            for (int i = 0; i < 3 * SM::kEpi; ++i) mbar_init(&rbars[i], 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -399,7 +410,7 @@ __device__ __forceinline__ void tc2_run(const CUtensorMap& tmA, const CUtensorMa
     } else {
         // ------------------------------------------------------------ epilogue (both CTAs)
         if constexpr (EPI == kEpiFused) {
-            tc2_fused_epilogue<BN>(tmY, tmR, p, smem, rbars + (warp - 2) * 3, epi_scratch, tfull, tempty, abort_flag,
+            tc2_fused_epilogue<BN, NEF>(tmY, tmR, p, smem, rbars + (warp - 2) * 3, epi_scratch, tfull, tempty, abort_flag,
                                    tmem_base, (int)rank, cluster_id, nclusters, num_tiles);
         } else {
         const int quarter = warp & 3;              // TMEM lanes [32 q, 32 q + 32)
@@ -523,11 +534,11 @@ __global__ void __launch_bounds__(kTc2Threads, 1)
     tc2_run<EPI, BN>(tmA, tmB, nullptr, nullptr, p);
 }
 
-template <int BN>
-__global__ void __launch_bounds__(kTc2Threads, 1)
+template <int BN, int NEF>
+__global__ void __launch_bounds__(Tc2Smem<BN, NEF>::kThreads, 1)
     gemm_i8_tc2_fused_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                              const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmR, TcParams p) {
-    tc2_run<kEpiFused, BN>(tmA, tmB, &tmY, &tmR, p);
+    tc2_run<kEpiFused, BN, NEF>(tmA, tmB, &tmY, &tmR, p);
 }
 
 }  // namespace w8a8

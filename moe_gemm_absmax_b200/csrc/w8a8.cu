@@ -128,11 +128,11 @@ int launch_tc(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st) {
 }
 
 // Pair-tile GEMM (cta_group::2, 256 x BN tiles over two SMs).
-template <int EPI, int BN>
+template <int EPI, int BN, int NEF = 0>
 int launch_tc2_bn(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st) {
-    using SM = Tc2Smem<BN, EPI == kEpiFused>;
+    using SM = Tc2Smem<BN, NEF>;
     const auto kern = [] {
-        if constexpr (EPI == kEpiFused) return gemm_i8_tc2_fused_kernel<BN>;
+        if constexpr (EPI == kEpiFused) return gemm_i8_tc2_fused_kernel<BN, NEF>;
         else return gemm_i8_tc2_kernel<EPI, BN>;
     }();
     int dev = 0;
@@ -140,7 +140,7 @@ int launch_tc2_bn(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st)
     if (dev < 0 || dev >= kMaxDevices) return W8A8_ERR_UNSUPPORTED;
     static int max_clusters[kMaxDevices] = {0};
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kTc2Threads, 1, 1);
+    cfg.blockDim = dim3(SM::kThreads, 1, 1);
     cfg.dynamicSmemBytes = SM::kBytes;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
@@ -245,10 +245,20 @@ int launch_tc2_g128(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t s
 
 template <int EPI>
 int launch_tc2(const int8_t* A, const int8_t* B, TcParams p, cudaStream_t st) {
-    const int bn = pick_tc2_bn(p.M, p.N, current_sms() / 2);
-    return bn == 160 ? launch_tc2_bn<EPI, 160>(A, B, p, st)
-         : bn == 144 ? launch_tc2_bn<EPI, 144>(A, B, p, st)
-                     : launch_tc2_bn<EPI, 256>(A, B, p, st);
+    const int clusters = current_sms() / 2;
+    const int bn = pick_tc2_bn(p.M, p.N, clusters);
+    if constexpr (EPI == kEpiFused) {
+        if (bn == 160) return launch_tc2_bn<EPI, 160, 16>(A, B, p, st);
+        if (bn == 144) return launch_tc2_bn<EPI, 144, 8>(A, B, p, st);
+        // 8 epilogue warps where four waves of 32 k blocks or more hide them, else 16
+        const int64_t tiles = (int64_t)((p.M + kTc2BM - 1) / kTc2BM) * ((p.N + 255) / 256);
+        return p.K >= 4096 && tiles >= 4 * clusters ? launch_tc2_bn<EPI, 256, 8>(A, B, p, st)
+                                                    : launch_tc2_bn<EPI, 256, 16>(A, B, p, st);
+    } else {
+        return bn == 160 ? launch_tc2_bn<EPI, 160>(A, B, p, st)
+             : bn == 144 ? launch_tc2_bn<EPI, 144>(A, B, p, st)
+                         : launch_tc2_bn<EPI, 256>(A, B, p, st);
+    }
 }
 
 // Tile width: the one with less work in its last wave (256 on ties).
