@@ -304,7 +304,10 @@ struct AttnCfg {
     static constexpr int U = ROW / 16;                       // 16-byte units of a row
     static constexpr int kScales = INT8 ? TT * 4 : 0;
     static constexpr int kStage = 2 * (TT * ROW + kScales);  // keys, values, their scales
-    static constexpr int kStages = kStage <= 4608 ? 4 : 2;
+    // (int8 rows of 64: three stages, so that a fourth CTA fits an SM -- its short
+    // tiles are bound by the latency of a warp's chain: 32 sequences of up to 16384,
+    // 8 heads, 84.5 -> 77 us against four stages and three CTAs)
+    static constexpr int kStages = kStage <= 4608 ? 3 : 2;
     static constexpr int kRing = kStages * kStage;           // a warp's
     // words of Q's fragments per lane and MMA k step: three planes of int8, or bf16
     static constexpr int kQWords = INT8 ? (NQ == 1 ? 6 : 12) : 2 * NQ;
@@ -312,9 +315,11 @@ struct AttnCfg {
     static constexpr int kQ = kQSteps * 32 * kQWords * 4;
     static constexpr int kJoin = kAttnWarps * QT * (D + 4) * 4;   // over the ring, between segments
     static constexpr int kBytes = kQ + (kAttnWarps * kRing > kJoin ? kAttnWarps * kRing : kJoin);
-    static constexpr int kMinB = (227 * 1024) / (kBytes + 2048) >= 3 && !(NQ == 2 && D == 256) ? 3
-                               : (227 * 1024) / (kBytes + 2048) >= 2                           ? 2
-                                                                                               : 1;
+    // CTAs an SM: what shared memory holds (some 2 KB more is static and reserved),
+    // less where the registers would spill
+    static constexpr int kFit = (227 * 1024) / (kBytes + 2048);
+    static constexpr int kMost = NQ == 1 ? 4 : (D == 256 ? 2 : 3);
+    static constexpr int kMinB = kFit < 1 ? 1 : (kFit < kMost ? kFit : kMost);
 };
 
 template <int D, bool INT8, int NQ>

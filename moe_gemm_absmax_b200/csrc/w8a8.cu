@@ -1662,7 +1662,7 @@ bool cache_shape_ok(int Hkv, int D, int64_t num_pages, int page_size) {
 // Up to 16 query heads share a pass over the cache.
 int attn_nq(int G) { return G > 8 ? 2 : 1; }
 constexpr int kAttnSms = 148;   // the work split's grid is fixed, so that workspace sizes are
-constexpr int kAttnMaxMinB = 3;
+constexpr int kAttnMaxMinB = 4;
 
 size_t attn_part_rows(int nq) { return (size_t)kAttnSms * kAttnMaxMinB * 2 * 8 * nq; }
 
