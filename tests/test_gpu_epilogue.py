@@ -127,6 +127,59 @@ def test_epilogue_leaves_the_rows_behind(M):
     assert bool((y[M:] == 7).all())
 
 
+# Outputs of more tiles than CTAs can share go to the pair tiles, in each of their widths and epilogues: 256 columns
+# with 16 epilogue warps, 160, 144, and 256 with 8 warps (many tiles of 32 k blocks or more).
+PAIRS = [(300, 64, 12808), (150, 144, 21536), (300, 64, 10408), (1030, 4096, 15368)]
+
+
+@pytest.mark.parametrize("M,K,N", PAIRS)
+def test_epilogue_pair_tiles(M, K, N):
+    x, qw, sw, bias, res = _case(M, K, N, 5)
+    for name in ACTS:
+        for b, r in ((bias, res), (bias, None), (None, res)):
+            _check(w8a8.linear_epilogue(x, qw, sw, bias=b, act=ACTS[name], residual=r), x, qw, sw, b, r, name)
+    assert torch.equal(w8a8.linear_epilogue(x, qw, sw), w8a8.linear(x, qw, sw))
+    # strided, in place, in a padded batch: nothing beside or behind the output is touched
+    want = w8a8.linear_epilogue(x, qw, sw, bias=bias, act=w8a8.ACT_SILU, residual=res)
+    wide = torch.full((M + 40, N + 24), 5.0, dtype=torch.bfloat16, device="cuda")
+    wide[:M, 8:8 + N] = res
+    wide_x = torch.full((M, K + 16), 3.0, dtype=torch.bfloat16, device="cuda")
+    wide_x[:, 8:8 + K] = x
+    y = wide[:M, 8:8 + N]
+    for _ in range(2):
+        y.copy_(res)
+        w8a8.linear_epilogue(wide_x[:, 8:8 + K], qw, sw, bias=bias, act=w8a8.ACT_SILU, residual=y, y=y)
+        assert torch.equal(y, want)
+    assert bool((wide[:, :8] == 5).all()) and bool((wide[:, 8 + N:] == 5).all()) and bool((wide[M:] == 5).all())
+    # non-finite values stay where they belong
+    bias[3], res[1, 5], res[M - 1, N - 1] = float("nan"), float("inf"), float("nan")
+    y = w8a8.linear_epilogue(x, qw, sw, bias, w8a8.ACT_RELU, res)
+    nan = torch.zeros_like(y, dtype=torch.bool)
+    nan[:, 3], nan[M - 1, N - 1] = True, True
+    assert torch.equal(torch.isnan(y), nan) and y[1, 5] == float("inf")
+    assert w8a8.get_device_error() == (w8a8.OK, 0)
+
+
+def test_epilogue_pair_tiles_captured_and_at_once():
+    cases = [_case(M, K, N, 6 + i) for i, (M, K, N) in enumerate(PAIRS[:3])]
+    calls = [lambda c=c, **kw: w8a8.linear_epilogue(*c[:3], c[3], w8a8.ACT_GELU_TANH, c[4], **kw) for c in cases]
+    want = [f() for f in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [[f(stream=s) for f, s in zip(calls, streams)] for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for row in got for a, b in zip(row, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ys = [f() for f in calls]
+    for c in cases:
+        c[0].copy_(torch.roll(c[0], 1, 0))
+        c[4].copy_(torch.roll(c[4], 1, 1))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, f()) for a, f in zip(ys, calls))
+
+
 def test_epilogue_non_finite_residual_and_bias():
     for M in (4, 20, 300):
         x, qw, sw, bias, res = _case(M, 256, 64, M)
