@@ -350,7 +350,7 @@ W8A8_API int w8a8_moe_g128_forward(const uint16_t* x, const uint16_t* logits, co
  *   v[m,n] = (float(sum_k qx[m,k] qw[n,k]) * sx[m]) * sw[n]   as w8a8_linear
  *   y[m,n] = bf16_rne( residual[m,n] + act( v[m,n] + bias[n] ) )
  * with one fp32 rounding for each product and sum; the activations are in
- * fp32, within 2^-18 of their value (beyond |v| = 80 they are 0 or v).
+ * fp32, within 2^-18 of their value for |v| < 8 and 2^-15 beyond.
  * Strides are in elements and multiples of 8 (ldx >= K, ldr >= N, ldy >= N);
  * elements of y between N and ldy are not touched.  y may be the residual
  * itself (same pointer and stride: the residual stream updated in place); it

@@ -161,7 +161,4 @@ __device__ __forceinline__ uint16_t epi_fused1(int acc, float sx, float sw, cons
     return float_to_bf16_bits(a);
 }
 
-// 16 bytes of the residual: coherent (it may be the output), past L1 (read once).
-__device__ __forceinline__ uint4 ld_residual16(const uint16_t* p) { return __ldcg(reinterpret_cast<const uint4*>(p)); }
-
 }  // namespace w8a8

@@ -24,7 +24,6 @@
 #include "common.cuh"
 #include "epilogue.cuh"
 #include "gemm_tc.cuh"
-#include "gemm_tc2.cuh"
 
 namespace w8a8 {
 

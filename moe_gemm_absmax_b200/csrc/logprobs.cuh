@@ -321,14 +321,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpArgs a)
     int part = 0;
     while (((batches - 1) >> part) >= kLpSlots) ++part;
     const int first = lo + tid;
-    if (edge >= 0) {
-        const uint32_t none = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;   // -inf
+    const uint32_t none = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;       // -inf
+    // in the order of indexes, as the first of equal values counts: the row's
+    // first window before the whole ones, its last behind them
+    auto take_edge = [&]() {
         uint4 q[kLpUnroll];
 #pragma unroll
         for (int i = 0; i < kLpUnroll; ++i) q[i] = make_uint4(none, none, none, none);
         q[0] = row.edge(edge);
         take(q, edge);
-    }
+    };
+    if (edge >= 0 && edge < first) take_edge();
     {
         // the next batch's loads are in flight while one is taken
         const int mine = hi > first ? (hi - first + kLpThreads - 1) / kLpThreads : 0;   // windows
@@ -357,7 +360,6 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpArgs a)
         }
         const int left = mine - full * kLpUnroll;
         if (left > 0) {
-            const uint32_t none = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;   // -inf
 #pragma unroll
             for (int i = 0; i < kLpUnroll; ++i) {
                 qa[i] = make_uint4(none, none, none, none);
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpArgs a)
             note(take(qa, first + batch * kStep));
         }
     }
+    if (edge >= first) take_edge();
     LpStat st = {m, 0.0f, 0.0f};
     {
         float a0, a1;

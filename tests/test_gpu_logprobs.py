@@ -86,6 +86,23 @@ def test_logprobs_ties_and_order():
         _check(x[5:6], tokens[:1], k)
 
 
+@pytest.mark.parametrize("dtype,per", [(torch.bfloat16, 8), (torch.float32, 4)])
+def test_logprobs_tie_with_the_rows_ragged_end(dtype, per):
+    """The largest value three times: in the second 16-byte window, in a later one, and behind the last whole one, which
+    the second window's thread takes as well."""
+    V = 400 * per + 3
+    x = torch.zeros((3, V), dtype=dtype, device="cuda")
+    for at in (per, 300 * per + 1, V - 1):
+        x[0, at] = 4.0
+    x[1, V - 1] = x[1, 299 * per] = 4.0
+    x[2, per + 2], x[2, V - 2] = 4.0, 5.0
+    tokens = torch.zeros(3, device="cuda", dtype=torch.int32)
+    for k in (1, 2, 3, 4):
+        _check(x, tokens[:1].expand(3).contiguous(), k)
+        for i in range(3):
+            _check(x[i:i + 1], tokens[:1], k)
+
+
 def test_logprobs_masked_rows():
     x = _logits(6, 3001, torch.float32)
     x[0, 10:] = -math.inf                                   # fewer left than alternatives asked for
