@@ -80,10 +80,8 @@ struct AppendCfg {
 template <int D, bool INT8>
 __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a) {
     constexpr int NV = AppendCfg<D, INT8>::NV, L = AppendCfg<D, INT8>::L;
-    const uint32_t row = blockIdx.x * (256 / L) + threadIdx.x / L;
-    const int l = threadIdx.x % L;
-    const int64_t t = row / (uint32_t)a.Hkv;
-    const int h = (int)(row - (uint32_t)t * (uint32_t)a.Hkv);
+    const int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+    const int l = threadIdx.x % L, h = blockIdx.y;
     uint4 x[2][NV] = {};
     int64_t slot = -1;
     if (t < a.T) {
@@ -124,24 +122,32 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a) {
         }
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) both = max_u16x2(both, __shfl_xor_sync(0xffffffffu, both, o));
+        float top[2] = {__uint_as_float(both << 16), __uint_as_float(both & 0xffff0000u)};
+        if (__any_sync(0xffffffffu, (both & 0xffffu) > 0x7f80u || (both >> 16) > 0x7f80u)) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const uint32_t w[4] = {x[s][0].x, x[s][0].y, x[s][0].z, x[s][0].w};
+                top[s] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    top[s] = fmaxf(top[s], fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+#pragma unroll
+                for (int o = L / 2; o > 0; o >>= 1) top[s] = fmaxf(top[s], __shfl_xor_sync(0xffffffffu, top[s], o));
+            }
+        }
+        // scale and reciprocal of the key by the even lanes, of the value by the odd
+        const QuantRow mine(l & 1 ? top[1] : top[0]);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const uint32_t w[4] = {x[s][0].x, x[s][0].y, x[s][0].z, x[s][0].w};
-            const uint32_t top = s ? both >> 16 : both & 0xffffu;
-            float m = __uint_as_float(top << 16), f[8];
+            const int from = (threadIdx.x & 30) + s;
+            const QuantRow q(__shfl_sync(0xffffffffu, mine.s, from), __shfl_sync(0xffffffffu, mine.rcp, from));
+            float f[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 f[2 * i] = __uint_as_float(w[i] << 16);
                 f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
             }
-            if (__any_sync(0xffffffffu, top > 0x7f80u)) {
-                m = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
-#pragma unroll
-                for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            }
-            const QuantRow q(m);
             uint32_t c[2];
             quant_codes<2>(f, q, c);
             if (slot >= 0) {

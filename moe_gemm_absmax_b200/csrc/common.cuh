@@ -392,6 +392,12 @@ struct QuantRow {
         zero = s == 0.0f;
         fast = fabsf(s) < INFINITY && fabsf(rcp) < 1.0e38f;
     }
+    // from the scale and its reciprocal, computed elsewhere by the above
+    __device__ __forceinline__ QuantRow(float scale, float reciprocal) : s(scale), rcp(reciprocal) {
+        rcp2 = f2_pack(rcp, rcp);
+        zero = s == 0.0f;
+        fast = fabsf(s) < INFINITY && fabsf(rcp) < 1.0e38f;
+    }
 };
 
 // Codes of 4W consecutive values v (|v| <= 127.25 s) under row quantizer r,

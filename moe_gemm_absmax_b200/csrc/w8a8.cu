@@ -1755,7 +1755,7 @@ int attn_clusters_d(int64_t units, int64_t cap, bool int8, int nq) {
 template <int D, bool INT8>
 int launch_append(const KvAppendArgs& a, cudaStream_t st) {
     constexpr int kRows = 256 / AppendCfg<D, INT8>::L;   // a CTA's
-    kv_append_kernel<D, INT8><<<dim3((unsigned)((a.T * a.Hkv + kRows - 1) / kRows), 1, 1), 256, 0, st>>>(a);
+    kv_append_kernel<D, INT8><<<dim3((unsigned)((a.T + kRows - 1) / kRows), (unsigned)a.Hkv, 1), 256, 0, st>>>(a);
     return last_launch_status();
 }
 }  // namespace
@@ -1773,7 +1773,6 @@ int w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ld
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 16) ||
         !aligned(v_scale, 16) || !aligned(slots, 8))
         return W8A8_ERR_INVALID_ARG;
-    if (T * Hkv > 0x7fffffffLL) return W8A8_ERR_UNSUPPORTED;
     KvAppendArgs a;
     a.k = {k, ldk, k_cache, k_scale};
     a.v = {v, ldv, v_cache, v_scale};
