@@ -563,16 +563,14 @@ def _row_stride(t, dtype, name, device, shape=None, ndim=2) -> int:
         raise TypeError(f"{name} must be a CUDA tensor on {device}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    size = t.shape
+    size, step = t.shape, t.stride()
     if len(size) != ndim or (shape is not None and size != shape):
         raise ValueError(f"{name} must have shape {tuple(shape) if shape is not None else f'({ndim} dims)'}, "
                          f"got {tuple(size)}")
-    step = t.stride()
-    n = 1
-    for i in range(ndim - 1, 0, -1):
-        if step[i] != n and size[i] != 1:
+    n = size[1] if ndim == 2 else size[1] * size[2]
+    if step[-1] != 1 or (ndim == 3 and step[1] != size[2]):   # strides of a dim of size 1 do not matter
+        if (size[-1] != 1 and step[-1] != 1) or (ndim == 3 and size[1] != 1 and step[1] != size[2]):
             raise ValueError(f"{name}: all but the first dim must be dense")
-        n *= size[i]
     return step[0] if size[0] > 1 else n
 
 
@@ -616,7 +614,8 @@ def linear_epilogue(x, qw, sw, bias=None, act: int = ACT_NONE, residual=None, y=
 def _cache_args(k_cache, v_cache, k_scale, v_scale, device):
     """Shape (pages, Hkv, page size, D) of a paged cache, int8 with scales or bf16 without, and its addresses."""
     dtype = torch.bfloat16 if k_scale is None else torch.int8
-    _need(k_cache, dtype, "k_cache", 4)
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise TypeError("k_cache must be a 4-D CUDA tensor")
     shape = k_cache.shape
     pk, pv = _on(k_cache, dtype, "k_cache", shape, device), _on(v_cache, dtype, "v_cache", shape, device)
     if k_scale is None:
