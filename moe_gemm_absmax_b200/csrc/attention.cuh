@@ -41,7 +41,7 @@
 // attn_join_kernel, which adds the parts in order.  Where a cluster's CTAs can
 // have a (sequence, head) to themselves with a few chunks each, they do, and
 // join through distributed shared memory: no search, workspace or second
-// kernel (one sequence of 1000, 4 heads, bf16: 7.7 -> 6.9 us).
+// kernel (one sequence of 1000, 4 heads, bf16: 7.7 -> 7.1 us).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -84,14 +84,15 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a) {
     const int l = threadIdx.x % L, h = blockIdx.y;
     uint4 x[2][NV] = {};
     int64_t slot = -1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // may overlap the kernel before it
     if (t < a.T) {
-        slot = __ldg(a.slots + t);
+        slot = __ldca(a.slots + t);
         const uint4* ks = reinterpret_cast<const uint4*>(a.k.x + t * a.k.ldx + (int64_t)h * D) + l;
         const uint4* vs = reinterpret_cast<const uint4*>(a.v.x + t * a.v.ldx + (int64_t)h * D) + l;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            x[0][i] = __ldg(ks + i * L);
-            x[1][i] = __ldg(vs + i * L);
+            x[0][i] = __ldca(ks + i * L);
+            x[1][i] = __ldca(vs + i * L);
         }
         if (slot >= 0 && (slot >> a.page_shift) >= a.num_pages) {
             record_error(W8A8_ERR_INVALID_ARG, (kKernelIdKvAppend << 16) | 1);
@@ -192,7 +193,7 @@ template <int D, bool INT8>
 constexpr int attn_tt() { return INT8 ? (D == 256 ? 16 : 32) : (D == 64 ? 32 : 16); }
 
 __device__ __forceinline__ int64_t attn_len(const AttnArgs& a, int b) {
-    const int64_t n = __ldg(a.lengths + b);
+    const int64_t n = __ldca(a.lengths + b);
     return n < 0 ? 0 : (n > a.cap ? a.cap : n);
 }
 
@@ -347,6 +348,10 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
     uint32_t* qs = reinterpret_cast<uint32_t*>(smem);         // Q's fragments: [step][word / 2][lane][2]
     float* so = reinterpret_cast<float*>(smem + Cfg::kQ);     // [warp][QT][D + 4], between segments
 
+    // may overlap the kernel before it, whose results (and whose reads of y and of the
+    // workspace) are complete only now (launched so, and with a plain stream order: one
+    // sequence of 1000, 4 heads, bf16, 6.8 / 7.2 us)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     // attn_join_kernel may launch; it waits for this grid before it reads the parts
     if (a.csize == 0) asm volatile("griddepcontrol.launch_dependents;");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -411,7 +416,7 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
         auto page_of = [&](int64_t tile) -> int {     // of the tile's token number `lane`; < 0: absent
             const int64_t t = tile * TT + lane;
             if (tile >= tile_end || lane >= TT || t >= len) return -1;
-            const int pg = __ldg(trow + (t >> a.page_shift));
+            const int pg = __ldca(trow + (t >> a.page_shift));
             if (pg < 0 || pg >= a.num_pages) {
                 bad = true;
                 return -1;
@@ -487,7 +492,7 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         w[i][e] = make_uint4(0, 0, 0, 0);
-                        if (has) w[i][e] = __ldg(reinterpret_cast<const uint4*>(qrow + 64 * i + 16 * c + 8 * e));
+                        if (has) w[i][e] = __ldca(reinterpret_cast<const uint4*>(qrow + 64 * i + 16 * c + 8 * e));
                         const uint32_t x[4] = {w[i][e].x, w[i][e].y, w[i][e].z, w[i][e].w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                 for (int i = 0; i < KL; ++i) {
                     if (i % kAttnWarps != warp) continue;
                     uint4 w = make_uint4(0, 0, 0, 0);
-                    if (has) w = __ldg(reinterpret_cast<const uint4*>(qrow + 32 * i + 8 * c));
+                    if (has) w = __ldca(reinterpret_cast<const uint4*>(qrow + 32 * i + 8 * c));
                     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -927,7 +932,7 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
     if (bad) record_error(W8A8_ERR_INVALID_ARG, (kKernelIdAttn << 16) | 1);
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < a.B; i += kAttnThreads)
-            if (__ldg(a.lengths + i) > a.cap) record_error(W8A8_ERR_INVALID_ARG, (kKernelIdAttn << 16) | 2);
+            if (__ldca(a.lengths + i) > a.cap) record_error(W8A8_ERR_INVALID_ARG, (kKernelIdAttn << 16) | 2);
 }
 
 // Joins the parts of the (sequence, head) units that several CTAs shared, and

@@ -130,7 +130,7 @@ struct LpRow {
     }
     // For a second look: through L1.
     __device__ __forceinline__ uint4 again(int w) const {
-        return whole(w) ? __ldg(reinterpret_cast<const uint4*>(at(w))) : edge(w);
+        return whole(w) ? __ldca(reinterpret_cast<const uint4*>(at(w))) : edge(w);
     }
     __device__ __forceinline__ static void unpack(const uint4& v, float (&x)[E]) {
         const uint32_t q[4] = {v.x, v.y, v.z, v.w};
@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpArgs a)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int w0 = (int)((int64_t)row.W * r / C), w1 = (int)((int64_t)row.W * (r + 1) / C);
 
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // may overlap the kernel before it
     // the given tokens' logits, in flight with the pass
     float xt = 0.0f;
     bool tok_ok = false;

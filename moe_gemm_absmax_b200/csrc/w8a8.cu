@@ -1710,25 +1710,27 @@ int launch_attn(AttnArgs a, cudaStream_t st) {
     const int64_t units = (int64_t)a.B * a.Hkv * a.qtiles;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute at[2];
+    pdl_config(cfg, at, true);
     a.csize = attn_clusters_of<D, INT8, NQ>(units, a.cap);
     if (a.csize > 0) {
         a.grid = (int)(units * a.csize);
         cfg.gridDim = dim3((unsigned)a.grid, 1, 1);
         cfg.blockDim = dim3(kAttnThreads, 1, 1);
         cfg.dynamicSmemBytes = Cfg::kBytes;
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = (unsigned)a.csize;
-        at[0].val.clusterDim.y = 1;
-        at[0].val.clusterDim.z = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = (unsigned)a.csize;
+        at[1].val.clusterDim.y = 1;
+        at[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
         return cuda_status(cudaLaunchKernelEx(&cfg, kern, a));
     }
     const int64_t most = units * ((a.cap + Cfg::CH - 1) / Cfg::CH);   // chunks, if every sequence were full
     a.grid = (int)(most < kAttnSms * Cfg::kMinB ? most : kAttnSms * Cfg::kMinB);
-    kern<<<(unsigned)a.grid, kAttnThreads, Cfg::kBytes, st>>>(a);
-    int rc = last_launch_status();
+    cfg.gridDim = dim3((unsigned)a.grid, 1, 1);
+    cfg.blockDim = dim3(kAttnThreads, 1, 1);
+    cfg.dynamicSmemBytes = Cfg::kBytes;
+    int rc = cuda_status(cudaLaunchKernelEx(&cfg, kern, a));
     if (rc != W8A8_OK) return rc;
     // few units have many parts each: more slices of their outputs, so that
     // more threads share the parts (down to a warp's worth of outputs a CTA)
@@ -1737,7 +1739,7 @@ int launch_attn(AttnArgs a, cudaStream_t st) {
     while (per_cta > 32 && units * (kItems / per_cta) < 4 * kAttnSms) per_cta /= 2;
     cfg.gridDim = dim3((unsigned)units, (unsigned)(kItems / per_cta), 1);
     cfg.blockDim = dim3(kAttnJoinThreads, 1, 1);
-    pdl_config(cfg, at, true);
+    cfg.dynamicSmemBytes = 0;
     return cuda_status(cudaLaunchKernelEx(&cfg, attn_join_kernel<D, Cfg::CH, NQ>, a, per_cta));
 }
 
@@ -1755,8 +1757,13 @@ int attn_clusters_d(int64_t units, int64_t cap, bool int8, int nq) {
 template <int D, bool INT8>
 int launch_append(const KvAppendArgs& a, cudaStream_t st) {
     constexpr int kRows = 256 / AppendCfg<D, INT8>::L;   // a CTA's
-    kv_append_kernel<D, INT8><<<dim3((unsigned)((a.T + kRows - 1) / kRows), (unsigned)a.Hkv, 1), 256, 0, st>>>(a);
-    return last_launch_status();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.T + kRows - 1) / kRows), (unsigned)a.Hkv, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    pdl_config(cfg, at, true);
+    return cuda_status(cudaLaunchKernelEx(&cfg, kv_append_kernel<D, INT8>, a));
 }
 }  // namespace
 
@@ -1886,13 +1893,13 @@ int w8a8_token_logprobs(const void* logits, int logits_f32, int64_t ld, const in
     cfg.gridDim = dim3((unsigned)(M * C), 1, 1);
     cfg.blockDim = dim3(kLpThreads, 1, 1);
     cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)C;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute at[2];
+    pdl_config(cfg, at, true);
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)C;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
     return cuda_status(logits_f32 ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<float>, a)
                                   : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<uint16_t>, a));
 }

@@ -85,3 +85,67 @@ def test_decode_step(B, int8):
         assert ((lp - lp0[:, 0]).abs() <= tl).all() and ((ent - ent0).abs() <= te).all()
         assert ((top - top0).abs() <= tl[:, None]).all() and torch.equal(top[:, 0], lp)
     assert w8a8.get_device_error() == (w8a8.OK, 0)
+
+
+@pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("lens", [[300], [5000, 1, 900] * 4])
+def test_operators_wait_for_what_is_before_them(lens, int8):
+    """Each operator behind a copy, a kernel and another stream's work that write its inputs, and before a kernel that
+    reads its outputs while the next call already waits to write them: captured and eager give the same."""
+    Hkv, G, D, V = 2, 4, 128, 20000
+    B, steps = len(lens), 6
+    c = Cache([n + steps for n in lens], Hkv, D, 16, int8, seed=7, junk=False)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    qs = torch.randn((steps, B, G * Hkv, D), generator=g, device="cuda").to(torch.bfloat16)
+    kvs = torch.randn((steps, 2, B, Hkv, D), generator=g, device="cuda").to(torch.bfloat16)
+    xs = torch.randn((steps, B, V), generator=g, device="cuda")
+    at = torch.arange(steps, device="cuda")[:, None] + torch.tensor(lens, device="cuda")[None]       # [steps, B]
+    slots_all = c.table.long().gather(1, (at // 16).T).T * 16 + at % 16
+    lengths_all = (at + 1).int()
+    q, kv, x = torch.zeros_like(qs[0]), torch.zeros_like(kvs[0]), torch.zeros_like(xs[0])
+    slots, lengths = torch.zeros_like(slots_all[0]), torch.zeros_like(lengths_all[0])
+    y = torch.zeros_like(q)
+    acc = torch.zeros((B, G * Hkv, D), device="cuda")
+    ent = torch.zeros(B, device="cuda")
+    k0, v0 = c.k.clone(), c.v.clone()
+    side = torch.cuda.Stream()
+
+    def run():
+        acc.zero_()
+        ent.zero_()
+        for i in range(steps):
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                slots.copy_(slots_all[i])
+                lengths.copy_(lengths_all[i])
+            kv.copy_(kvs[i])                                   # a copy
+            torch.cuda.current_stream().wait_stream(side)
+            w8a8.kv_append(kv[0], kv[1], c.k, c.v, slots, k_scale=c.ks, v_scale=c.vs)
+            torch.mul(qs[i], 1.0, out=q)                       # a kernel
+            w8a8.paged_attention(q, c.k, c.v, c.table, lengths, k_scale=c.ks, v_scale=c.vs, y=y)
+            acc.add_(y)
+            torch.mul(xs[i], 1.0, out=x)
+            ent.add_(w8a8.token_logprobs(x)[1])
+
+    run()
+    torch.cuda.synchronize()
+    want = acc.clone(), ent.clone(), c.k.clone(), c.v.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(3):
+        c.k.copy_(k0)
+        c.v.copy_(v0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((acc, ent, c.k, c.v), want))
+    each = torch.zeros_like(acc)                               # and one at a time
+    c.k.copy_(k0)
+    c.v.copy_(v0)
+    for i in range(steps):
+        w8a8.kv_append(kvs[i, 0], kvs[i, 1], c.k, c.v, slots_all[i].contiguous(), k_scale=c.ks, v_scale=c.vs)
+        torch.cuda.synchronize()
+        each.add_(w8a8.paged_attention(qs[i], c.k, c.v, c.table, lengths_all[i].contiguous(), k_scale=c.ks, v_scale=c.vs))
+        torch.cuda.synchronize()
+    assert torch.equal(each, want[0])
+    assert w8a8.get_device_error() == (w8a8.OK, 0)
