@@ -270,6 +270,16 @@ __device__ __forceinline__ uint4 ld_stream_16(const void* p) {
                  : "l"(p));
     return v;
 }
+// The same for data of the kernel before, behind griddepcontrol.wait: not a
+// non-coherent load, which could be moved above the wait.
+__device__ __forceinline__ uint4 ld_stream_16_coherent(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
 
 // ---------------------------------------------------------------------------
 // Project exponential, identical op for op to the oracle's: Cody & Waite

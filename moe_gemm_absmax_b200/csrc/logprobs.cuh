@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpArgs a)
         const T* at = row.at(first);
         auto load = [&](uint4 (&q)[kLpUnroll]) {
 #pragma unroll
-            for (int i = 0; i < kLpUnroll; ++i) q[i] = ld_stream_16(at + i * kLpThreads * E);
+            for (int i = 0; i < kLpUnroll; ++i) q[i] = ld_stream_16_coherent(at + i * kLpThreads * E);
             at += kStep * E;
         };
         int batch = 0;
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpArgs a)
 #pragma unroll
             for (int i = 0; i < kLpUnroll; ++i) {
                 qa[i] = make_uint4(none, none, none, none);
-                if (i < left) qa[i] = ld_stream_16(at + i * kLpThreads * E);
+                if (i < left) qa[i] = ld_stream_16_coherent(at + i * kLpThreads * E);
             }
             note(take(qa, first + batch * kStep));
         }
