@@ -60,7 +60,8 @@ __device__ __forceinline__ float lp_ex2(float x) {
 // e = 2^t.  Where there is no logit above -inf, s = 0 and m is the lowest
 // finite value, so that nothing is ever subtracted from -inf; the distance
 // to a new maximum is cut at -1e4, where e^d is 0, so that no 0 * inf
-// arises.  NaN and +inf reach s through e.
+// arises (an element's own distance: take, below).  NaN and +inf reach s
+// through e.
 struct LpStat {
     float m, s, u;
 };
@@ -294,7 +295,11 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(LpArgs a)
             for (int i = kLpUnroll - 1; i >= 0; --i)
                 if (LpFast<T>::holds(tops[i], top)) best = wb + i * kLpThreads;
         }
-        const uint64_t nm = f2_pack(-m, -m), l2 = f2_pack(kLog2e, kLog2e);
+        // a distance below a maximum of more than FLT_MAX / log2 e could pass fp32's range
+        // as t, and t e = -inf * 0 would be NaN: past 1e38 two values are equal or 1e31
+        // apart, so e is 1 or 0 and t e is 0 whatever the factor
+        const float lg = m > 1.0e38f ? 1.0f : kLog2e;
+        const uint64_t nm = f2_pack(-m, -m), l2 = f2_pack(lg, lg);
 #pragma unroll
         for (int i = 0; i < kLpUnroll; ++i) {
             float x[E];
