@@ -278,6 +278,9 @@ __device__ __forceinline__ float attn_ex2(float x) {
     return y;
 }
 
+// Exponent of the power of two that brings values of up to x to [0, 2).
+__device__ __forceinline__ int attn_unit(float x) { return min(max((int)(__float_as_uint(x) >> 23) - 127, -126), 126); }
+
 // 16 bytes to shared memory, the first `bytes` of them from global memory, zeros behind.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -553,12 +556,12 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
 
         float o[NQ][OT][4];
         float m[NQ], l[NQ];
-        int oe[NQ];               // int8: o is in units of 2^oe (of sum p v)
+        float big[NQ];            // int8: the largest p times value scale; o is in units of 2^attn_unit(big)
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             m[n] = -INFINITY;
             l[n] = 0.0f;
-            oe[n] = -127;
+            big[n] = 0.0f;
 #pragma unroll
             for (int i = 0; i < OT; ++i)
 #pragma unroll
@@ -726,11 +729,13 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                     }
                     um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 1));
                     um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 2));
-                    // the unit never falls below the old one's place in the new reference, so fac stays below 2
-                    const float old = __uint_as_float((uint32_t)(oe[n] + 127) << 23) * corr;
-                    const int en = min(max((int)(__float_as_uint(fmaxf(um, old)) >> 23) - 127, -126), 126);
-                    fac[n] = corr * __uint_as_float((uint32_t)min(max(oe[n] - en + 127, 0), 254) << 23);
-                    oe[n] = en;
+                    // the unit follows the largest of all so far in the new reference, so fac stays below 2 (from
+                    // the old unit's place instead, it fell by one with every rise of the maximum, however
+                    // small, and o overflowed behind a hundred of them)
+                    const float now = fmaxf(um, big[n] * corr);
+                    const int eo = attn_unit(big[n]), en = attn_unit(now);
+                    fac[n] = corr * __uint_as_float((uint32_t)min(max(eo - en + 127, 0), 254) << 23);
+                    big[n] = now;
                     const float unit = __uint_as_float((uint32_t)(127 - en) << 23);
 #pragma unroll
                     for (int j = 0; j < NT8; ++j) {
@@ -834,7 +839,7 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                 sl[warp][8 * n + g] = l[n];
             }
             float un = 1.0f;
-            if (INT8) un = __uint_as_float((uint32_t)(max(oe[n], -126) + 127) << 23);
+            if (INT8) un = __uint_as_float((uint32_t)(attn_unit(big[n]) + 127) << 23);
             const float u0f = __shfl_sync(0xffffffffu, un, 8 * c), u1f = __shfl_sync(0xffffffffu, un, 8 * c + 4);
             // tile i covers d = 8 DPL (i / (DPL / 2)) + DPL g + 2 (i % (DPL / 2)), + 1
             float* dst = so + (warp * QT + 8 * n + 2 * c) * (D + 4);
