@@ -399,9 +399,9 @@ W8A8_API int w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, i
  *   l_t = scale * (q . k_t),  p_t = exp(l_t - max l),
  *   y = bf16_rne( sum_t p_t v_t / sum_t p_t )   for t < lengths[b]
  * Scores, maxima, sums and outputs are held in fp32; int8 codes meet the query
- * as integers (its head scaled by a power of two to 21 bits), probabilities
- * times value scales round to fp16 (2^-11) below that, with a bf16 cache to two
- * bf16 (2^-16).  A NaN or infinity in a query head, or in a key or value that is
+ * as integers (its head scaled by a power of two to 21 bits); probabilities
+ * times value scales are the sum of two fp16 (2^-22, but not below 2^-39 of the
+ * head's largest), with a bf16 cache probabilities of two bf16 (2^-16).  A NaN or infinity in a query head, or in a key or value that is
  * attended to, makes the outputs that it reaches NaN or infinite; what lies in
  * the cache beyond a sequence's length is never used.  A sequence of length 0
  * (or less) gives zeros.  A length beyond max_pages * page_size is cut there,

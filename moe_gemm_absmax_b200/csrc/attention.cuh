@@ -26,11 +26,14 @@
 // to 2^-20 of it); with up to 8 query heads the first two planes are the upper
 // and lower half of one MMA's 16 rows.  The int32 sums are exact and join in
 // fp32.  Keys' scales multiply the scores, values' scales the probabilities,
-// which a running power of two per query brings to [0, 2) before they round
-// to fp16 (2^-11, an eighth of the output's own rounding); the values' codes
-// become fp16 exactly (the byte, offset to unsigned, under the exponent of
-// 1024, less 1152).  bf16 cache: bf16 MMAs, with the probabilities as the sum
-// of two bf16 (2^-16).
+// which a running power of two per query brings to [0, 2^15) and which then are
+// the sum of two fp16: good to 2^-22, and below 2^-17 of the loudest token's to
+// 2^-39 of that (a single fp16 lost the quiet tokens wherever the loud ones'
+// codes are 0; 64 sequences of up to 8191, 8 x 4 heads of 128: 114 us with two
+// parts, 111 with one, 129 with two bf16, which have no such end but take two
+// more instructions a pair of codes).  The values' codes become fp16 exactly
+// (the byte, offset to unsigned, under the exponent of 1024, less 1152).  bf16
+// cache: bf16 MMAs, with the probabilities as the sum of two bf16 (2^-16).
 //
 // Work split: chunks of 4 tiles (one per warp), ordered by (sequence, head),
 // in equal contiguous shares over a fixed grid, whatever the lengths are (a
@@ -278,8 +281,8 @@ __device__ __forceinline__ float attn_ex2(float x) {
     return y;
 }
 
-// Exponent of the power of two that brings values of up to x to [0, 2).
-__device__ __forceinline__ int attn_unit(float x) { return min(max((int)(__float_as_uint(x) >> 23) - 127, -126), 126); }
+// Exponent of the power of two that values of up to x are divided by: x comes to [2^14, 2^15).
+__device__ __forceinline__ int attn_unit(float x) { return max((int)(__float_as_uint(x) >> 23) - 127 - 14, -126); }
 
 // 16 bytes to shared memory, the first `bytes` of them from global memory, zeros behind.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -678,7 +681,7 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                     vsc[j] = make_float2(__uint_as_float(vx.x), __uint_as_float(vx.y));
                 }
             }
-            uint32_t pf[NQ][NT8], pl[NQ][NT8];        // fp16 pairs; bf16: high and low parts
+            uint32_t pf[NQ][NT8], pl[NQ][NT8];        // pairs of fp16 or bf16: high and low parts
             float fac[NQ];
             bool rescale = false;
 #pragma unroll
@@ -719,7 +722,7 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                     }
                 l[n] = l[n] * corr + sum;
                 if (INT8) {
-                    // probabilities times the values' scales, brought to [0, 2) by a power of two
+                    // probabilities times the values' scales, brought to [0, 2^15) by a power of two
                     float um = 0.0f;
 #pragma unroll
                     for (int j = 0; j < NT8; ++j) {
@@ -739,8 +742,12 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                     const float unit = __uint_as_float((uint32_t)(127 - en) << 23);
 #pragma unroll
                     for (int j = 0; j < NT8; ++j) {
-                        const __half2 hv = __floats2half2_rn(x[j][0] * unit, x[j][1] * unit);
+                        const float u0 = x[j][0] * unit, u1 = x[j][1] * unit;
+                        const __half2 hv = __floats2half2_rn(u0, u1);
+                        const float2 hf = __half22float2(hv);
+                        const __half2 lv = __floats2half2_rn(u0 - hf.x, u1 - hf.y);
                         pf[n][j] = *reinterpret_cast<const uint32_t*>(&hv);
+                        pl[n][j] = *reinterpret_cast<const uint32_t*>(&lv);
                     }
                 } else {
                     fac[n] = corr;
@@ -804,6 +811,8 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                             for (int n = 0; n < NQ; ++n) {
                                 mma_f16_16816(o[n][(i * VW + w) * 2], a0, a1, a2, a3, pf[n][j], pf[n][j + 1]);
                                 mma_f16_16816(o[n][(i * VW + w) * 2 + 1], b0, b1, b2, b3, pf[n][j], pf[n][j + 1]);
+                                mma_f16_16816(o[n][(i * VW + w) * 2], a0, a1, a2, a3, pl[n][j], pl[n][j + 1]);
+                                mma_f16_16816(o[n][(i * VW + w) * 2 + 1], b0, b1, b2, b3, pl[n][j], pl[n][j + 1]);
                             }
                         } else {
                             const uint32_t a0 = __byte_perm(vr[0][w], vr[1][w], 0x5410);

@@ -34,6 +34,15 @@ def _held(cache, scale, b, n, table):
     return x.transpose(0, 1).flatten(1, 2)[:, :n]
 
 
+def _floor(cache, scale, b, n, table, p):
+    """What the sum of two fp16 may lose, [Hkv, 1, D]: u = p s is scaled so that the largest of a head lies in
+    [2^14, 2^15); fp16's smallest step is 2^-24, so the lower part is off by up to 2^-25, which is 2^-39 of that largest
+    u, for each token that has a code at d."""
+    codes = _held(cache, None, b, n, table).abs()
+    u = _held(torch.ones_like(cache[..., :1]), scale, b, n, table) * p            # [Hkv, n, 1]
+    return (2.0 ** -39 * u.amax(dim=1, keepdim=True) * codes.sum(dim=1, keepdim=True))
+
+
 def _at(t, page):
     return t // page, t % page
 
@@ -64,4 +73,62 @@ def test_attention_maximum_that_rises_slowly(D, G):
     tol = (2.0 ** -8 + 2.0 ** -16 + n / 4 / 32 * 2.0 ** -22) * want
     bad = (y.double() - want).abs() > tol
     assert not bad.any(), (int(bad.sum()), y[bad][:4], want[:4])
+    assert w8a8.get_device_error() == (w8a8.OK, 0)
+
+
+@pytest.mark.parametrize("D,G", [(64, 3), (128, 4), (128, 12), (256, 6), (256, 16)])
+@pytest.mark.parametrize("n", [40, 700, 20000])
+def test_attention_value_scales_far_apart(n, D, G):
+    """One token's values are 2^8 to 2^24 times as loud as the others', but its codes are zero from d = 16 on: there the
+    others decide, each of them far below the loudest."""
+    page, loud = 16, (8, 14, 17, 20, 24)
+    c, s, table, lengths = _int8(len(loud), n, 2, D, page, seed=D + G)
+    for b, e in enumerate(loud):
+        for t in (3, n - 1, n // 2)[:1 + b % 3]:
+            pg, at = _at(t, page)
+            pg = int(table[b, pg])
+            c[1][pg, :, at, 16:] = 0
+            s[1][pg, :, at] = 2.0 ** e
+    q = torch.zeros((len(loud), 2 * G, D), dtype=torch.bfloat16, device="cuda")      # every token weighs the same
+    y = w8a8.paged_attention(q, c[0], c[1], table, lengths, k_scale=s[0], v_scale=s[1])
+    for b in range(len(loud)):
+        v = _held(c[1], s[1], b, n, table)
+        want, size = v.mean(dim=1)[:, None], v.abs().mean(dim=1)[:, None]
+        # bf16's rounding; probability times scale to 2^-20, sums of n terms in fp32 (2^-23 each, pairwise by lanes
+        # and warps: no more than n of them)
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -20 + n * 2.0 ** -23) * size + _floor(c[1], s[1], b, n, table, 1.0 / n)
+        bad = (y[b].double().view(2, G, D) - want).abs() > tol
+        assert not bad.any(), (b, int(bad.sum()), float(((y[b].double().view(2, G, D) - want).abs() / tol).max()))
+    assert w8a8.get_device_error() == (w8a8.OK, 0)
+
+
+@pytest.mark.parametrize("D,G", [(64, 3), (128, 4), (128, 12), (256, 6)])
+@pytest.mark.parametrize("n", [40, 700, 20000])
+def test_attention_quiet_tokens_count_together(n, D, G):
+    """A first token that takes nearly all of the probability and whose values are zero from d = 16 on: there the many
+    others, of probability 2^-20 to 2^-30 each, are all that the output holds."""
+    page = 16
+    c, s, table, lengths = _int8(3, n, 2, D, page, seed=n)
+    c[0].zero_()
+    s[0].fill_(1.0)
+    first = table[:, 0].long()
+    c[0][first, :, 0, 0] = 64
+    c[1][first, :, 0, 16:] = 0
+    q = torch.zeros((3, 2 * G, D), dtype=torch.bfloat16, device="cuda")
+    for b, e in enumerate((20, 25, 30)):
+        q[b, :, 0] = e                                       # the first token's score: 64 e scale = e log 2
+    scale = math.log(2) / 64
+    y = w8a8.paged_attention(q, c[0], c[1], table, lengths, scale=scale, k_scale=s[0], v_scale=s[1])
+    for b, e in enumerate((20, 25, 30)):
+        v = _held(c[1], s[1], b, n, table)
+        p = torch.full((n,), 2.0 ** -e, dtype=torch.float64, device="cuda")
+        p[0] = 1.0
+        p /= p.sum()
+        want = (p[None, :, None] * v).sum(dim=1)[:, None]
+        size = (p[None, :, None] * v.abs()).sum(dim=1)[:, None]
+        # a score of e log2 units is off by its three roundings and scale's (2^-22 e together), through the exponential
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -20 + 2.0 ** -22 * e + n * 2.0 ** -23) * size \
+            + _floor(c[1], s[1], b, n, table, p[:, None])
+        bad = (y[b].double().view(2, G, D) - want).abs() > tol
+        assert not bad.any(), (b, int(bad.sum()), float(((y[b].double().view(2, G, D) - want).abs() / tol).max()))
     assert w8a8.get_device_error() == (w8a8.OK, 0)
