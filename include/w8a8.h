@@ -402,8 +402,9 @@ W8A8_API int w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, i
  * as integers (its head scaled by a power of two to 21 bits); probabilities
  * times value scales are the sum of two fp16 (2^-22, but not below 2^-39 of the
  * head's largest), with a bf16 cache probabilities of two bf16 (2^-16).  A NaN or infinity in a query head, or in a key or value that is
- * attended to, makes the outputs that it reaches NaN or infinite; what lies in
- * the cache beyond a sequence's length is never used.  A sequence of length 0
+ * attended to, makes the outputs that it reaches NaN or infinite (a score of
+ * -inf has probability 0; where all of a head's are, its outputs are NaN); what
+ * lies in the cache beyond a sequence's length is never used.  A sequence of length 0
  * (or less) gives zeros.  A length beyond max_pages * page_size is cut there,
  * and positions of a page number outside [0, num_pages) count as absent;
  * either records W8A8_ERR_INVALID_ARG in the device error word.

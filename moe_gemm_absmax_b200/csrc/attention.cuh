@@ -48,6 +48,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <float.h>
 
 #include "common.cuh"
 
@@ -706,6 +707,9 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                 }
 #pragma unroll
                 for (int j = 0; j < NT8; ++j) mx = fmaxf(mx, fmaxf(x[j][0], x[j][1]));
+                // m = -inf: no token so far.  Tokens with scores of -inf alone: m is the lowest finite value, every
+                // probability 0, and the output 0 / 0
+                if (there) mx = fmaxf(mx, -FLT_MAX);
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const float mn = fmaxf(m[n], mx);
@@ -888,7 +892,7 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                 *reinterpret_cast<float4*>(so + qh * (D + 4) + d) = acc;
                 if (d == 0) cml[qh] = make_float2(mm, ll);
             } else if (whole) {
-                const float r = ll == 0.0f ? 0.0f : 1.0f / ll;
+                const float r = mm == -INFINITY ? 0.0f : 1.0f / ll;
                 *reinterpret_cast<uint2*>(a.y + ((int64_t)b * a.Hq + q0 + qh) * D + d) =
                     make_uint2(cvt_bf16x2(acc.x * r, acc.y * r), cvt_bf16x2(acc.z * r, acc.w * r));
             } else {
@@ -937,7 +941,7 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                 acc.z += v[p].z * f;
                 acc.w += v[p].w * f;
             }
-            const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+            const float inv = mm == -INFINITY ? 0.0f : 1.0f / ll;
             *reinterpret_cast<uint2*>(a.y + ((int64_t)b * a.Hq + q0 + qh) * D + d) =
                 make_uint2(cvt_bf16x2(acc.x * inv, acc.y * inv), cvt_bf16x2(acc.z * inv, acc.w * inv));
         }
@@ -1039,7 +1043,7 @@ __global__ void __launch_bounds__(kAttnJoinThreads) attn_join_kernel(AttnArgs a,
         for (int j = 1; j < ng; ++j) add(rml[j * per_cta + item], racc[j * per_cta + item]);
     }
     if (qh >= nq) return;
-    const float r = ll == 0.0f ? 0.0f : 1.0f / ll;
+    const float r = mm == -INFINITY ? 0.0f : 1.0f / ll;
     *reinterpret_cast<uint2*>(a.y + ((int64_t)b * a.Hq + q0 + qh) * D + d) =
         make_uint2(cvt_bf16x2(acc.x * r, acc.y * r), cvt_bf16x2(acc.z * r, acc.w * r));
 }

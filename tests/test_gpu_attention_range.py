@@ -132,3 +132,37 @@ def test_attention_quiet_tokens_count_together(n, D, G):
         bad = (y[b].double().view(2, G, D) - want).abs() > tol
         assert not bad.any(), (b, int(bad.sum()), float(((y[b].double().view(2, G, D) - want).abs() / tol).max()))
     assert w8a8.get_device_error() == (w8a8.OK, 0)
+
+
+@pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("n", [1, 300, 20000])
+def test_attention_scores_of_minus_infinity(n, int8):
+    """Keys that are infinite: where each of a head's scores is -inf the outputs are NaN, as the formula's; where one
+    score is finite they are its value; absent tokens remain absent."""
+    D, page, Hkv, G = 64, 16, 2, 3
+    c, s, table, lengths = _int8(4, n, Hkv, D, page, seed=5)
+    c[0][..., 0] = 100
+    s[1].fill_(1.0)
+    q = torch.randn((4, Hkv * G, D), generator=_gen(6), device="cuda").to(torch.bfloat16)
+    if int8:
+        q[..., 1:] = 0
+        q[..., 0] = -q[..., 0].abs() - 1                     # every score of an infinite scale is -inf
+        s[0][:, 0] = math.inf                                # of the first key-value head
+    else:
+        c = [x.to(torch.bfloat16) for x in c]
+        s = [None, None]
+        q[..., 0] = -q[..., 0].abs() - 1
+        c[0][:, 0, :, 0] = math.inf
+    pg, at = _at(n - 1, page)
+    pg = int(table[1, pg])
+    if int8:
+        s[0][pg, 0, at] = 1.0
+    else:
+        c[0][pg, 0, at, 0] = 1.0
+    lengths[2] = 0
+    table[3] = -1
+    y = w8a8.paged_attention(q, c[0], c[1], table, lengths, k_scale=s[0], v_scale=s[1])
+    assert w8a8.get_device_error()[0] == w8a8.ERR_INVALID_ARG          # the absent pages
+    assert bool(torch.isnan(y[0, :G]).all()) and bool(torch.isfinite(y[0, G:]).all())
+    assert torch.equal(y[1, :G], c[1][pg, 0, at].to(torch.bfloat16).expand(G, D)) and bool(torch.isfinite(y[1]).all())
+    assert not y[2:].any()
