@@ -398,16 +398,18 @@ W8A8_API int w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, i
  *   y  bf16 [B, Hq, D], dense; may not overlap the inputs
  *   l_t = scale * (q . k_t),  p_t = exp(l_t - max l),
  *   y = bf16_rne( sum_t p_t v_t / sum_t p_t )   for t < lengths[b]
- * Scores, maxima, sums and outputs are held in fp32; int8 codes meet the query
- * as integers (its head scaled by a power of two to 21 bits); probabilities
- * times value scales are the sum of two fp16 (2^-22, but not below 2^-39 of the
- * head's largest), with a bf16 cache probabilities of two bf16 (2^-16).  A NaN or infinity in a query head, or in a key or value that is
- * attended to, makes the outputs that it reaches NaN or infinite (a score of
- * -inf has probability 0; where all of a head's are, its outputs are NaN); what
- * lies in the cache beyond a sequence's length is never used.  A sequence of length 0
- * (or less) gives zeros.  A length beyond max_pages * page_size is cut there,
- * and positions of a page number outside [0, num_pages) count as absent;
- * either records W8A8_ERR_INVALID_ARG in the device error word.
+ * Scores, maxima, sums and outputs are held in fp32.  int8 cache: codes meet
+ * the query as integers (its head scaled by a power of two to 31 bits, to 23
+ * where Hq / Hkv > 8), and probabilities times value scales are the sum of two
+ * fp16 (2^-22, but not below 2^-39 of the head's largest).  bf16 cache:
+ * probabilities are the sum of two bf16 (2^-16).  A NaN or infinity in a query
+ * head, or in a key or value that is attended to, makes the outputs that it
+ * reaches NaN or infinite (a score of -inf has probability 0; where all of a
+ * head's are, its outputs are NaN); what lies in the cache beyond a sequence's
+ * length is never used.  A sequence of length 0 (or less) gives zeros.  A length
+ * beyond max_pages * page_size is cut there, and positions of a page number
+ * outside [0, num_pages) count as absent; either records W8A8_ERR_INVALID_ARG
+ * in the device error word.
  * The context is split over the GPU and its parts are joined in a fixed order:
  * the same call gives the same bits again.  1 <= B <= 4096.  `ws` belongs to one
  * call at a time: calls that overlap on the GPU need workspaces of their own.

@@ -21,10 +21,13 @@
 //     tokens and pairs them across tokens with byte permutes
 //
 // int8 cache.  Scores are int8 MMAs on the codes themselves: the query's head
-// is scaled by a power of two to 21-bit integers and cut into three planes of
-// signed 7 bits (exact but for elements 2^-12 below its largest, which round
-// to 2^-20 of it); with up to 8 query heads the first two planes are the upper
-// and lower half of one MMA's 16 rows.  The int32 sums are exact and join in
+// is scaled by a power of two to integers and cut into planes of signed 8 bits.
+// With up to 8 query heads a plane fills half of an MMA's 16 rows: two MMAs
+// take four planes, 31 bits (exact but for elements 2^-22 below the head's
+// largest, which round to 2^-30 of it).  With more heads a plane is an MMA of
+// its own: three of them, 23 bits (2^-14, 2^-22; a fourth would cost 64
+// sequences of up to 8191, 8 x 16 heads of 128, 165 -> 193 us).  The int32 sums
+// are exact and join in
 // fp32.  Keys' scales multiply the scores, values' scales the probabilities,
 // which a running power of two per query brings to [0, 2^15) and which then are
 // the sum of two fp16: good to 2^-22, and below 2^-17 of the loudest token's to
@@ -323,8 +326,9 @@ struct AttnCfg {
     // 8 heads, 84.5 -> 77 us against four stages and three CTAs)
     static constexpr int kStages = kStage <= 4608 ? 3 : 2;
     static constexpr int kRing = kStages * kStage;           // a warp's
-    // words of Q's fragments per lane and MMA k step: three planes of int8, or bf16
-    static constexpr int kQWords = INT8 ? (NQ == 1 ? 6 : 12) : 2 * NQ;
+    // words of Q's fragments per lane and MMA k step: kPlanes of int8, or bf16
+    static constexpr int kPlanes = NQ == 1 ? 4 : 3;
+    static constexpr int kQWords = INT8 ? 2 * NQ * kPlanes : 2 * NQ;
     static constexpr int kQSteps = INT8 ? D / 32 : D / 16;
     static constexpr int kQ = kQSteps * 32 * kQWords * 4;
     static constexpr int kJoin = kAttnWarps * QT * (D + 4) * 4;   // over the ring, between segments
@@ -347,7 +351,8 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
     constexpr int VW = VB / 4;                        // words per value load
     constexpr int OT = D / 16;                        // output tiles of 16 d
     constexpr int DPL = INT8 ? VB : VB / 2;           // d's per value load and lane
-    constexpr int QW = Cfg::kQWords;
+    constexpr int QW = Cfg::kQWords, PL = Cfg::kPlanes, kQBits = 8 * PL - 2;
+    constexpr int QM = NQ == 1 ? PL / 2 : PL;         // MMAs of a step of int8 scores
 
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float sm[kAttnWarps][QT], sl[kAttnWarps][QT];
@@ -508,34 +513,36 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                     }
                 amax = fmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                // amax in [2^e, 2^(e+1)): integers q 2^(19-e), below 2^20; NaN and infinities pass through the scale
-                const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100);
-                const float up = __uint_as_float((uint32_t)(min(19 - e, 127) + 127) << 23);
-                qscale[n] *= amax < INFINITY ? __uint_as_float((uint32_t)(e - 19 + 127) << 23) : __int_as_float(0x7fc00000);
+                // amax in [2^e, 2^(e+1)): integers below 2^kQBits; NaN and infinities pass through the scale
+                const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -90);
+                const float up = __uint_as_float((uint32_t)(kQBits - 1 - e + 127) << 23);
+                qscale[n] *= amax < INFINITY ? __uint_as_float((uint32_t)(e - (kQBits - 1) + 127) << 23) : __int_as_float(0x7fc00000);
 #pragma unroll
                 for (int i = 0; i < KL; ++i) {
                     if (i % kAttnWarps != warp) continue;
 #pragma unroll
                     for (int st = 0; st < 2; ++st) {         // MMA step 2 i + st: d = 64 i + 16 c + 8 st + [0, 8)
                         const uint32_t x[4] = {w[i][st].x, w[i][st].y, w[i][st].z, w[i][st].w};
-                        int p[3][8];
+                        int p[PL][8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const float f = __uint_as_float(k & 1 ? x[k / 2] & 0xffff0000u : x[k / 2] << 16);
-                            const int v = __float2int_rn(f * up);
-                            p[0][k] = (v + 8192) >> 14;
-                            const int r = v - (p[0][k] << 14);
-                            p[1][k] = (r + 64) >> 7;
-                            p[2][k] = r - (p[1][k] << 7);
+                            int v = __float2int_rn(f * up);
+#pragma unroll
+                            for (int pl = PL - 1; pl > 0; --pl) {      // digits in [-128, 128)
+                                p[pl][k] = (int)(int8_t)v;
+                                v = (v - p[pl][k]) >> 8;
+                            }
+                            p[0][k] = v;
                         }
 #pragma unroll
-                        for (int pl = 0; pl < 3; ++pl)
+                        for (int pl = 0; pl < PL; ++pl)
 #pragma unroll
                             for (int hf = 0; hf < 2; ++hf) {
                                 const uint32_t v = pack4_s8(p[pl][4 * hf], p[pl][4 * hf + 1], p[pl][4 * hf + 2], p[pl][4 * hf + 3]);
-                                // NQ = 1: words (a0, a1, a2, a3) = planes 0, 1, 0, 1; then plane 2.
+                                // NQ = 1: words (a0, a1, a2, a3) = planes 0, 1, 0, 1; then 2, 3, 2, 3.
                                 // NQ = 2: plane by plane (a0, a1, a2, a3)
-                                const int word = NQ == 1 ? (pl < 2 ? 2 * hf + pl : 4 + hf) : 4 * pl + 2 * hf + n;
+                                const int word = NQ == 1 ? 4 * (pl / 2) + 2 * hf + pl % 2 : 4 * pl + 2 * hf + n;
                                 qs[(((2 * i + st) * (QW / 2) + word / 2) * 32 + lane) * 2 + (word & 1)] = v;
                             }
                     }
@@ -580,14 +587,13 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
             // ---- scores
             float s[NQ][NT8][2];
             if (INT8) {
-                int hi[NQ][NT8][4], lo[NQ][NT8][4], mid[NQ == 2 ? NT8 : 1][4];
+                int acc[QM][NT8][4];   // of a pair of planes (NQ = 1) or a plane
 #pragma unroll
-                for (int j = 0; j < NT8; ++j)
+                for (int x = 0; x < QM; ++x)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        hi[0][j][k] = lo[0][j][k] = 0x4B400000;   // the bits of 1.5 * 2^23: sums come out as floats
-                        if (NQ == 2) mid[j % (NQ == 2 ? NT8 : 1)][k] = 0x4B400000;
-                    }
+                    for (int j = 0; j < NT8; ++j)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[x][j][k] = 0x4B400000;   // the bits of 1.5 * 2^23: sums come out as floats
 #pragma unroll
                 for (int i = 0; i < KL; ++i) {
                     uint4 kr[NT8];
@@ -606,21 +612,15 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
 #pragma unroll
                         for (int j = 0; j < NT8; ++j) {
                             const uint32_t bk[2] = {st ? kr[j].z : kr[j].x, st ? kr[j].w : kr[j].y};
-                            const uint32_t a0[4] = {q[0], q[1], q[2], q[3]};
-                            mma_s8_16832(hi[0][j], a0, bk);
-                            if (NQ == 1) {
-                                const uint32_t a1[4] = {q[4], 0u, q[5], 0u};
-                                mma_s8_16832(lo[0][j], a1, bk);
-                            } else {
-                                const uint32_t a1[4] = {q[4 % QW], q[5 % QW], q[6 % QW], q[7 % QW]};
-                                const uint32_t a2[4] = {q[8 % QW], q[9 % QW], q[10 % QW], q[11 % QW]};
-                                mma_s8_16832(mid[j % (NQ == 2 ? NT8 : 1)], a1, bk);
-                                mma_s8_16832(lo[0][j], a2, bk);
+#pragma unroll
+                            for (int x = 0; x < QM; ++x) {
+                                const uint32_t aq[4] = {q[4 * x % QW], q[(4 * x + 1) % QW], q[(4 * x + 2) % QW], q[(4 * x + 3) % QW]};
+                                mma_s8_16832(acc[x][j], aq, bk);
                             }
                         }
                     }
                 }
-                // planes join: |sums| < 2^22, so sum + 1.5 * 2^23 is exact in fp32 and its bits were added up
+                // planes join: |sums| <= 2^22, so sum + 1.5 * 2^23 is exact in fp32 and its bits were added up
                 auto value = [](int bits) { return __fsub_rn(__int_as_float(bits), 12582912.0f); };
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
@@ -628,10 +628,13 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<D, INT8, NQ>::kMinB)) p
                     for (int j = 0; j < NT8; ++j)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int p0 = hi[0][j][2 * n + e];
-                            const int p1 = NQ == 1 ? hi[0][j][2 + e] : mid[j % (NQ == 2 ? NT8 : 1)][2 * n + e];
-                            const int p2 = lo[0][j][2 * n + e];
-                            s[n][j][e] = __fmaf_rn(16384.0f, value(p0), __fmaf_rn(128.0f, value(p1), value(p2)));
+                            float sum = 0.0f;
+#pragma unroll
+                            for (int pl = PL - 1; pl >= 0; --pl) {
+                                const float p = value(NQ == 1 ? acc[pl / 2][j][2 * (pl & 1) + e] : acc[pl % QM][j][2 * n + e]);
+                                sum = pl == PL - 1 ? p : __fmaf_rn((float)(1u << (8 * (PL - 1 - pl))), p, sum);
+                            }
+                            s[n][j][e] = sum;
                         }
             } else {
                 float acc[NT8][4];

@@ -166,3 +166,35 @@ def test_attention_scores_of_minus_infinity(n, int8):
     assert bool(torch.isnan(y[0, :G]).all()) and bool(torch.isfinite(y[0, G:]).all())
     assert torch.equal(y[1, :G], c[1][pg, 0, at].to(torch.bfloat16).expand(G, D)) and bool(torch.isfinite(y[1]).all())
     assert not y[2:].any()
+
+
+@pytest.mark.parametrize("D,G", [(64, 3), (128, 4), (128, 12), (256, 6), (256, 16)])
+@pytest.mark.parametrize("n", [40, 700, 20000])
+def test_attention_query_elements_far_apart(n, D, G):
+    """One query element 2^10 to 2^18 times as large as the others, which meets zero codes: the others decide the scores,
+    and each of them counts with all of its digits."""
+    page, large = 16, (10, 12, 14, 16, 18)
+    c, s, table, lengths = _int8(len(large), n, 2, D, page, seed=n + D)
+    c[0][..., 5] = 0
+    s[0] *= 1.0 / 64
+    q = torch.randn((len(large), 2 * G, D), generator=_gen(G), device="cuda")
+    for b, e in enumerate(large):
+        q[b, :, 5] = 2.0 ** e * 1.5
+    q = q.to(torch.bfloat16)
+    y = w8a8.paged_attention(q, c[0], c[1], table, lengths, k_scale=s[0], v_scale=s[1])
+    for b in range(len(large)):
+        k, v = _held(c[0], s[0], b, n, table), _held(c[1], s[1], b, n, table)
+        qb = q[b].double().view(2, G, D)
+        l = torch.einsum("hgd,htd->hgt", qb, k) * D ** -0.5
+        p = torch.softmax(l, dim=2)
+        want, size = torch.einsum("hgt,htd->hgd", p, v), torch.einsum("hgt,htd->hgd", p, v.abs())
+        # a score's error: elements rounded to 2^-30 of the largest (2^-22 beyond 8 heads), the sum's three joins, the products with scale and
+        # key scale and the subtraction of the maximum, 2^-24 each of what has been summed up
+        part = torch.einsum("hgd,htd->hgt", qb.abs(), k.abs()).amax(dim=2, keepdim=True) * D ** -0.5
+        small = 2.0 ** (-30 if G <= 8 else -22) * qb.abs().amax(dim=2, keepdim=True) * k.abs().sum(dim=2).amax(dim=1)[:, None, None] * D ** -0.5
+        dl = small + 8 * 2.0 ** -24 * part + 2.0 ** -21
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -20 + n * 2.0 ** -23 + 2 * dl) * size \
+            + (2.0 ** -39 * p.amax(dim=2, keepdim=True) * 1.5 * _held(c[1], None, b, n, table).abs().sum(dim=1)[:, None])
+        bad = (y[b].double().view(2, G, D) - want).abs() > tol
+        assert not bad.any(), (b, int(bad.sum()), float(((y[b].double().view(2, G, D) - want).abs() / tol).max()))
+    assert w8a8.get_device_error() == (w8a8.OK, 0)
