@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 
 import torch
@@ -519,21 +520,31 @@ ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
 def _placed(fn):
     """Runs fn with the device of its first tensor current and, where a stream is given, on that stream: what fn
     allocates then belongs to the stream that uses it, so the caching allocator cannot hand it on too early.  fn gets
-    the raw stream as its last argument."""
+    the raw stream as raw_stream; callers give stream=, and see that in the signature."""
+    params = list(inspect.signature(fn).parameters.values())
+    name = params[0].name
+    shown = [p for p in params if p.name != "raw_stream"]
+    shown.append(inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None))
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kwargs):
+    def call(*args, stream=None, **kwargs):
+        if not args and name not in kwargs:
+            raise TypeError(f"{fn.__name__}() missing 1 required positional argument: '{name}'")
+        first = args[0] if args else kwargs[name]
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise TypeError(f"{fn.__name__}: the first argument must be a CUDA tensor")
+            raise TypeError(f"{name} must be a CUDA tensor")
         index = first.get_device()
         if stream is None and index == torch._C._cuda_getDevice():
-            return fn(first, *args, raw_stream=_raw_stream(index), **kwargs)
+            return fn(*args, raw_stream=_raw_stream(index), **kwargs)
         if stream is None:
             with torch.cuda.device(index):
-                return fn(first, *args, raw_stream=_raw_stream(index), **kwargs)
+                return fn(*args, raw_stream=_raw_stream(index), **kwargs)
         if stream.device != first.device:
             raise ValueError("stream is on another device than the tensors")
         with torch.cuda.stream(stream):
-            return fn(first, *args, raw_stream=stream.cuda_stream, **kwargs)
+            return fn(*args, raw_stream=stream.cuda_stream, **kwargs)
+
+    call.__signature__ = inspect.Signature(shown)
     return call
 
 
