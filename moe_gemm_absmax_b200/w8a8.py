@@ -568,6 +568,15 @@ def _on(t, dtype, name, shape, device):
     return t.data_ptr()
 
 
+def _caller_ws(ws, device):
+    """Address and bytes of a workspace that the caller gave."""
+    if not isinstance(ws, torch.Tensor) or ws.device != device:
+        raise TypeError(f"ws must be a CUDA tensor on {device}")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _row_stride(t, dtype, name, device, shape=None, ndim=2) -> int:
     """Row stride of a tensor whose rows (all but the first dim) are dense."""
     if not isinstance(t, torch.Tensor) or t.device != device:
@@ -614,9 +623,13 @@ def linear_epilogue(x, qw, sw, bias=None, act: int = ACT_NONE, residual=None, y=
     else:
         ldy = _row_stride(y, torch.bfloat16, "y", dev, (M, N))
     if ws is None:
-        ws = _bytes(_linear_ws(M, N, K), dev)
+        nws = _linear_ws(M, N, K)
+        ws = _bytes(nws, dev)
+        pws = ws.data_ptr()
+    else:
+        pws, nws = _caller_ws(ws, dev)
     _check(lib().w8a8_linear_epilogue(x.data_ptr(), ldx, pw, ps, pb, act, pr, ldr, y.data_ptr(), ldy, M, N, K,
-                                      ws.data_ptr(), ws.numel(), raw_stream), "w8a8_linear_epilogue")
+                                      pws, nws, raw_stream), "w8a8_linear_epilogue")
     return y
 
 
@@ -686,13 +699,14 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, scale: float | No
         py = y.data_ptr()
     else:
         py = _on(y, torch.bfloat16, "y", (B, Hq, D), dev)
-    max_pages, pws, nws = block_table.shape[1], None, 0
+    max_pages, pws = block_table.shape[1], None
     if ws is None:
         nws = _attention_ws(B, Hq, Hkv, D, pks is not None, page, max_pages)
         if nws:
             ws = _bytes(nws, dev)
-    if ws is not None:
-        pws, nws = ws.data_ptr(), ws.numel()
+            pws = ws.data_ptr()
+    else:
+        pws, nws = _caller_ws(ws, dev)
     _check(lib().w8a8_paged_attention(q.data_ptr(), ldq, pkc, pvc, pks, pvs, block_table.data_ptr(), ld_table,
                                       _on(lengths, torch.int32, "lengths", (B,), dev), py, B, Hq, Hkv, D, pages, page,
                                       max_pages, D ** -0.5 if scale is None else scale, pws, nws, raw_stream),

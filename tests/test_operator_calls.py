@@ -65,3 +65,29 @@ def test_calls_by_name(side):
                 *w8a8.token_logprobs(logits, tokens, 3)]
     assert all(torch.equal(a, b) for a, b in zip(by_name, by_place))
     assert all(torch.equal(a, b) for a, b in zip(held, cache.values()))
+
+
+@pytest.mark.gpu
+def test_workspaces_from_the_caller():
+    """A workspace that the kernels cannot use is refused; any type of tensor that is large enough serves."""
+    x, qw, sw, kv, cache, at, _, _ = _inputs()
+    w8a8.kv_append(**kv, **cache)
+    table = torch.arange(3, dtype=torch.int32, device="cuda").repeat(1, 2000)     # wide enough for shares and a join
+    need = w8a8.paged_attention_workspace_size(1, 6, 2, 64, True, 8, table.shape[1])
+    assert need > 0
+    lin = lambda ws: w8a8.linear_epilogue(x, qw, sw, ws=ws)
+    att = lambda ws: w8a8.paged_attention(**{**at, "block_table": table}, **cache, ws=ws)
+    for call, n in ((lin, w8a8.linear_workspace_size(5, 128, 256)), (att, need)):
+        want = call(None)
+        n = max(n, 256)
+        for ws in (torch.empty(n, dtype=torch.uint8), [0] * n, "ws"):
+            with pytest.raises(TypeError, match="ws must be a CUDA tensor"):
+                call(ws)
+        with pytest.raises(ValueError, match="ws must be contiguous"):
+            call(torch.empty((n, 2), dtype=torch.uint8, device="cuda")[:, 0])
+        with pytest.raises(w8a8.W8A8Error):
+            call(torch.empty(n // 2, dtype=torch.uint8, device="cuda"))
+        for dtype in (torch.uint8, torch.float32):
+            assert torch.equal(call(torch.empty(n // dtype.itemsize, dtype=dtype, device="cuda")), want)
+    torch.cuda.synchronize()
+    assert w8a8.get_device_error() == (w8a8.OK, 0)
