@@ -349,8 +349,10 @@ W8A8_API int w8a8_moe_g128_forward(const uint16_t* x, const uint16_t* logits, co
  *   y  bf16 [M, N], row stride ldy
  *   v[m,n] = (float(sum_k qx[m,k] qw[n,k]) * sx[m]) * sw[n]   as w8a8_linear
  *   y[m,n] = bf16_rne( residual[m,n] + act( v[m,n] + bias[n] ) )
- * with one fp32 rounding for each product and sum; the activations are in
- * fp32, within 2^-18 of their value for |v| < 8 and 2^-15 beyond.
+ * with one fp32 rounding for each product and sum.  The activations are in
+ * fp32: for |v| < 8 SiLU and GELU are within 2^-18 of their value and GELU_TANH
+ * within 2^-16, all of them within 2^-15 beyond; values below 2^-110 may come
+ * out as 0.
  * Strides are in elements and multiples of 8 (ldx >= K, ldr >= N, ldy >= N);
  * elements of y between N and ldy are not touched.  y may be the residual
  * itself (same pointer and stride: the residual stream updated in place); it

@@ -22,9 +22,12 @@ struct EpiFused {
 
 // Activations on two values at a time (sm_100 adds and multiplies pairs of
 // fp32 in one instruction).  1 / (1 + e^-t) from ex2.approx and rcp.approx,
-// good to 2 ulp each, which leaves it within 2^-20 of its value, 1/4096 of a
-// bf16 rounding step.  Far left e^-t overflows to infinity and the quotient is
-// 0, the limit.
+// good to 2 ulp each; the exponent's roundings, 2^-24 of it each, come out as
+// that part of e^-t times its size, so that the value is within 2^-19 of the
+// true one for |t| < 8 and 2^-16 for |t| < 88, where e^-t leaves fp32.  (SiLU's
+// t is v; GELU-tanh's is 1.6 v + 0.07 v^3 with four roundings, 49 at v = -8:
+// 2^-16.5.)  All of that is far below bf16's half step, 2^-9.  Further left e^-t
+// overflows to infinity and the quotient is 0, the limit.
 __device__ __forceinline__ float epi_ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
