@@ -32,8 +32,8 @@
 // which a running power of two per query brings to [0, 2^15) and which then are
 // the sum of two fp16: good to 2^-22, and below 2^-17 of the loudest token's to
 // 2^-39 of that (a single fp16 lost the quiet tokens wherever the loud ones'
-// codes are 0; 64 sequences of up to 8191, 8 x 4 heads of 128: 114 us with two
-// parts, 111 with one, 129 with two bf16, which have no such end but take two
+// codes are 0; 64 sequences of up to 8191, 8 x 4 heads of 128: 116 us with two
+// parts, 112 with one, 130 with two bf16, which have no such end but take two
 // more instructions a pair of codes).  The values' codes become fp16 exactly
 // (the byte, offset to unsigned, under the exponent of 1024, less 1152).  bf16
 // cache: bf16 MMAs, with the probabilities as the sum of two bf16 (2^-16).
@@ -47,7 +47,7 @@
 // attn_join_kernel, which adds the parts in order.  Where a cluster's CTAs can
 // have a (sequence, head) to themselves with a few chunks each, they do, and
 // join through distributed shared memory: no search, workspace or second
-// kernel (one sequence of 1000, 4 heads, bf16: 7.7 -> 7.1 us).
+// kernel (one sequence of 1000, 4 heads, bf16: 7.6 -> 6.9 us).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -323,7 +323,7 @@ struct AttnCfg {
     static constexpr int kStage = 2 * (TT * ROW + kScales);  // keys, values, their scales
     // (int8 rows of 64: three stages, so that a fourth CTA fits an SM -- its short
     // tiles are bound by the latency of a warp's chain: 32 sequences of up to 16384,
-    // 8 heads, 84.5 -> 77 us against four stages and three CTAs)
+    // 8 x 4 heads, 89 -> 81 us against four stages and three CTAs)
     static constexpr int kStages = kStage <= 4608 ? 3 : 2;
     static constexpr int kRing = kStages * kStage;           // a warp's
     // words of Q's fragments per lane and MMA k step: kPlanes of int8, or bf16

@@ -16,11 +16,13 @@
 // The alternatives come out of the same pass without a list per thread.  Any
 // k disjoint groups of elements have k maxima, so the k-th largest of the
 // groups' maxima bounds the row's k-th largest from below.  Here a group is
-// two threads' elements (128 groups, which puts the bound at about the
-// k-th to 1.15 k-th largest for k <= 32), and only the threads whose own
-// maximum reaches the bound (about k of 256) have their elements read again,
-// from L2, a warp at a time.  What reaches the bound is ranked by counting.
-// Keys order by value, then lower index.
+// four threads' elements (64 groups, which puts the bound at the k-th largest
+// for small k, at about the 24th for k = 20 and the 44th for k = 32: in random
+// order 64 (ln 64 - ln(64 - k)) elements reach k of the groups).  Of the threads
+// whose own maximum reaches the bound only the parts of their share (16 to a
+// thread) whose maximum does are read again, from L2, dealt out over the CTA.
+// What reaches the bound is ranked by counting.  Keys order by value, then lower
+// index.
 #pragma once
 
 #include <cooperative_groups.h>

@@ -1672,12 +1672,17 @@ size_t attn_part_rows(int nq) { return (size_t)kAttnSms * kAttnMaxMinB * 2 * 8 *
 //
 // Clusters serve where that leaves a CTA few chunks; how few, goes by how much
 // of the GPU they fill (shares would fill all of it, but pay for the search and
-// the join).  8 heads of 128, int8, shares / clusters: 4 sequences of up to 1000
-// 9.6 / 8.5 us, of 4000 15.0 / 13.0; 16 of 2000 (8 chunks a CTA) 21.6 / 19.4, of
-// 4000 (16) 27.3 / 33.2; 64 of 1000 (8 chunks, one CTA a unit) 37.3 / 32.1, 256
-// of 2000 (16) 133 / 127.  Where a CTA fills an SM (D = 256, bf16), clusters of 8
-// do not pack (4 sequences of 500: 9.7 / 13.7 us, by fours 9.2), and many units a
-// CTA wait for one another's first loads (256 of 1000: 123 / 133).
+// the join).  8 x 4 heads of 128, int8, shares / clusters: 4 sequences of up to
+// 1000 9.5 / 8.3 us, of 4000 15.0 / 13.2; 16 of 2000 (8 chunks a CTA) 22.0 / 19.9,
+// of 4000 (16) 28.0 / 34.6; 64 of 1000 (8 chunks, one CTA a unit) 38.9 / 33.2, 256
+// of 2000 (16) 141 / 135.5.  Where a CTA fills an SM (D = 256, bf16), clusters of 8
+// do not pack (4 sequences of 500: shares 9.7 us, clusters of 8 13.7, of 4 9.2),
+// and many units a CTA wait for one another's first loads (256 of 1000, 8 x 4
+// heads: 225 / 245).
+//
+// The longest context that the table allows decides, as the host does not know
+// the lengths: under a table of 32768 positions the same contexts take the shares
+// (16 sequences of up to 500: 9.5 us under a tight table, 11.9 under that one).
 int attn_clusters(int64_t units, int64_t chunks, int minb) {
     const int64_t slots = (int64_t)kAttnSms * minb;
     int C = 8;
